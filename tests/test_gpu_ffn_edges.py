@@ -1,0 +1,74 @@
+"""GPU parity of the feed-forward operators at their edges: values that are no
+numbers and values at the ends of the types' ranges, against 64 bits
+(tests/ffn_ref.py derives the bounds)."""
+import zlib
+
+import pytest
+
+import tiled_dense_gemm_06_amd as tlg
+from tiled_dense_gemm_06_amd import _native as nat
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import ffn_ref as R  # noqa: E402
+
+T16 = [torch.float16, torch.bfloat16]
+CONFIGS = [-1] + [c for c in range(32) if nat.tlg_ffn_config_name(c)]
+
+
+def config_name(c):
+    return "auto" if c < 0 else nat.tlg_ffn_config_name(c)
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+def gen_for(dev, *key):
+    return torch.Generator(device=dev).manual_seed(zlib.crc32(repr(key).encode()))
+
+
+def served(fn):
+    """fn(), or None where a forced kernel does not serve the problem."""
+    try:
+        return fn()
+    except tlg.TlgError as e:
+        if e.status == nat.TLG_ERROR_NOT_SUPPORTED:
+            return None
+        raise
+
+
+@pytest.mark.parametrize("config", CONFIGS, ids=config_name)
+@pytest.mark.parametrize("t", T16, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("shape", [(300, 513, 259), (70, 77, 8), (130, 512, 130), (9, 13, 1)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_backward_infinity_in_the_last_channel(dev, shape, t, config):
+    """An infinite gradient of one token's last output makes that token's dX,
+    and the last channels' weight gradients, infinite (not NaN), and leaves the
+    other tokens and channels as they are. Inputs of the token and weights of
+    the channel are positive, so every term that meets the infinity agrees."""
+    M, K, N = shape
+    print(f"infinity {shape} {t} {config_name(config)}", flush=True)
+    g = gen_for(dev, *shape)
+    X = R.exact_ints(M, K, g, dev, t)
+    Wg, Wu = (R.exact_ints(N, K, g, dev, t) for _ in range(2))
+    G, U = (torch.randint(1, 4, (M, N), generator=g, device=dev).to(t) for _ in range(2))
+    dH = R.exact_ints(M, N, g, dev, t)
+    m = M // 2
+    X[m], Wg[N - 1], Wu[N - 1] = 1, 2, 1
+    clean = served(lambda: tlg.gated_ffn_backward(dH, X, Wg, Wu, G, U, act="relu", config=config))
+    if clean is None:
+        pytest.skip("not served by this kernel")
+    dH[m, N - 1] = float("inf")
+    dX, dWg, dWu = tlg.gated_ffn_backward(dH, X, Wg, Wu, G, U, act="relu", config=config)
+    torch.cuda.synchronize()
+    assert bool((dX[m] == float("inf")).all()), dX[m]
+    assert bool((dWg[N - 1] == float("inf")).all()) and bool((dWu[N - 1] == float("inf")).all())
+    others = torch.arange(M, device=dev) != m
+    assert torch.equal(dX[others], clean[0][others])
+    assert torch.equal(dWg[:N - 1], clean[1][:N - 1]) and torch.equal(dWu[:N - 1], clean[2][:N - 1])

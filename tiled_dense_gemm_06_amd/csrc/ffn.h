@@ -45,9 +45,10 @@ struct FfnProduct {
 hipError_t launch_ffn_general(const FfnProduct &p, hipStream_t stream);
 
 // A product for the pipelined kernel. K's first kmain elements are loaded in
-// 16-byte chunks (a multiple of the chunk), the rest one by one; ext_a and
-// ext_b are the readable elements of a row of a column-layout operand (ks !=
-// 1). splits > 1: the tiles past the first `whole` are cut into that many
+// 16-byte chunks, the rest (fewer than two chunks) one by one: kmain is a
+// multiple of the chunk where a row-layout operand has elements past it that
+// are not zero. ext_a and ext_b are the readable elements of a row of a
+// column-layout operand (ks != 1). splits > 1: the tiles past the first `whole` are cut into that many
 // parts each, whose sums go through `part`, min(M, BM) x BN x 4 bytes a tile
 // and part.
 struct FfnPanelCall {

@@ -5,6 +5,7 @@
 
 #include "context.h"
 #include "ffn.h"
+#include "ffn_panel.h"
 #include "tlg.h"
 
 namespace {
@@ -347,10 +348,9 @@ int64_t plan_workspace(Sizes z) {
 }
 
 // What the pipelined kernel's loads cover of K, or -1 where it cannot serve
-// the problem. Row-layout operands are loaded in whole 16-byte chunks of K;
-// column-layout ones in whole rows, where a chunk that crosses the end of a
-// row (its length no multiple of 8) reads into the next, so the last row is
-// staged instead. (dG and dU have zeros up to their pitch.)
+// the problem. Row-layout operands are loaded in whole 16-byte chunks of K,
+// column-layout ones in whole rows of k (pcol_kmain). (dG and dU have zeros up
+// to their pitch.)
 int64_t panel_kmain(const FfnProduct &p) {
     const bool i8 = p.type == tlg::FFN_I8, acol = p.A[0].ks != 1 || p.mode == tlg::FFN_PAIR;
     const int64_t eb = i8 ? 1 : 2;
@@ -363,7 +363,7 @@ int64_t panel_kmain(const FfnProduct &p) {
         if (p.C[o] && 128 * p.ldc[o] * 4 > kMaxOffset) return -1;
     if (bcol) {
         if (p.N < 8) return -1;
-        return p.N % 8 ? p.K - 1 : p.K;
+        return tlg::pcol_kmain(p.K, p.N, p.mode == tlg::FFN_SUM2);
     }
     return p.K / (16 / eb) * (16 / eb);
 }

@@ -85,6 +85,19 @@ TLG_PHD int pcol_frag(int x0, int t, int lane) {
     return pcol_offset<BX>(k, x / 8) + 2 * (x % 8);
 }
 
+// How many of the K k's of a product with a column-layout operand the loads
+// cover; the others, eight at most, are staged one by one. A column-layout
+// chunk that crosses the end of its row (`cols` elements, no multiple of 8)
+// reads into the next row, so the last row is staged. Against a column-layout
+// operand that is all: both are masked by single rows of k. A row-layout one is
+// masked by whole chunks of eight, so it stops at a whole chunk: an element
+// past kmain that came with its chunk would meet zeros, and an infinity times
+// zero is NaN.
+TLG_PHD int64_t pcol_kmain(int64_t K, int64_t cols, bool against_rows) {
+    if (cols % 8 == 0) return K;
+    return against_rows ? (K - 1) / 8 * 8 : K - 1;
+}
+
 // ---- gate and up side by side ----
 // A gated tile's BN rows of B alternate between Wg and Wu in runs of half a
 // wave's block, so that a wave holds both products of the same outputs: row r
