@@ -72,3 +72,29 @@ def test_backward_infinity_in_the_last_channel(dev, shape, t, config):
     others = torch.arange(M, device=dev) != m
     assert torch.equal(dX[others], clean[0][others])
     assert torch.equal(dWg[:N - 1], clean[1][:N - 1]) and torch.equal(dWu[:N - 1], clean[2][:N - 1])
+
+
+@pytest.mark.parametrize("t", T16, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh", "relu"])
+def test_gates_far_from_zero(dev, name, t):
+    """Past |g| = 256 every activation is g or 0 and its slope 1 or 0, up to the
+    largest finite value of the type: both gradients are exact."""
+    far = [256.0, 1000.0, 2.0 ** 14, float(torch.finfo(t).max)]
+    if t == torch.bfloat16:
+        far += [2.0 ** 62, 2.0 ** 64, 2.0 ** 80, 2.0 ** 120]
+    row = torch.tensor(far + [-v for v in far], device=dev).to(t)
+    n = 64
+    G = row.repeat(n // len(row))[None].repeat(5, 1)
+    G[2:] = G[2:].flip(1)
+    print(f"far gates {name} {t}", flush=True)
+    on = (G > 0).double()
+    eye, zero = torch.eye(n, dtype=t, device=dev), torch.zeros(n, n, dtype=t, device=dev)
+    U, dH = torch.full_like(G, 2), torch.full_like(G, 0.5)
+    one = torch.ones(5, n, dtype=t, device=dev)
+    _, Gk, _ = tlg.gated_ffn(G, eye, zero, act=name, save=True)
+    dg = tlg.gated_ffn_backward(dH, one, eye, zero, G, U, act=name)[0]
+    du = tlg.gated_ffn_backward(dH, one, zero, eye, G, U, act=name)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(Gk, G)
+    assert torch.equal(dg, on.to(t))
+    assert torch.equal(du, (G.double() * on * 0.5).to(t))

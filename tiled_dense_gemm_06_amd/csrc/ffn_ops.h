@@ -167,7 +167,8 @@ __device__ __forceinline__ float ffn_act_grad(float g, float *slope) {
         return g * cdf;
     } else if constexpr (ACT == TLG_ACT_GELU_TANH) {
         const float p = ffn_sigmoid(kGeluC * (g + kGeluA * g * g * g)), v = g * p;
-        *slope = p + v * (1.0f - p) * kGeluC * (1.0f + 3.0f * kGeluA * g * g);
+        // (past the range of g^2, v (1 - p) is zero: no infinity may meet it)
+        *slope = p + v * (1.0f - p) * kGeluC * (1.0f + 3.0f * kGeluA * fminf(g * g, 1e30f));
         return v;
     } else {
         *slope = g > 0.0f ? 1.0f : 0.0f;
