@@ -98,3 +98,68 @@ def test_gates_far_from_zero(dev, name, t):
     assert torch.equal(Gk, G)
     assert torch.equal(dg, on.to(t))
     assert torch.equal(du, (G.double() * on * 0.5).to(t))
+
+
+def ranged_case(kind, M, K, N, dev):
+    """fp16 inputs whose dG and dU lie outside fp16's range while the gradients lie inside."""
+    t = torch.float16
+    g = gen_for(dev, kind, M, K, N)
+    dh, u, x, w = {"large": (256, 300, 0.005, 0.005), "small": (1e-6, 2e-2, 30, 300), "mixed": (1e-3, 1e-3, 30, 1)}[kind]
+    normal = lambda r, c, s: (torch.randn(r, c, generator=g, device=dev) * s).to(t)  # noqa: E731
+    X, Wg, Wu = normal(M, K, x), normal(N, K, w), normal(N, K, w)
+    G, U, dH = normal(M, N, 1), normal(M, N, u), normal(M, N, dh)
+    if kind == "mixed":  # one channel ten million times the others
+        U[:, 0] = 1e4
+    return X, Wg, Wu, G, U, dH
+
+
+@pytest.mark.parametrize("config", CONFIGS, ids=config_name)
+@pytest.mark.parametrize("kind", ["large", "small", "mixed"])
+@pytest.mark.parametrize("shape", [(300, 264, 200), (130, 77, 90), (40, 5, 33)], ids=lambda s: "x".join(map(str, s)))
+def test_backward_past_the_range_of_fp16(dev, shape, kind, config):
+    """dG and dU carry one rounding (u) and the activation's error, and 2^-38 of
+    the largest |dH U| or |dH G| at most; the sums K 2^-24 of their magnitudes, the results
+    one rounding more (half a subnormal step near zero)."""
+    M, K, N = shape
+    t = torch.float16
+    name = ["silu", "gelu", "gelu_tanh", "relu"][(M + config) % 4]
+    print(f"range {shape} {kind} {name} {config_name(config)}", flush=True)
+    X, Wg, Wu, G, U, dH = ranged_case(kind, M, K, N, dev)
+    got = served(lambda: tlg.gated_ffn_backward(dH, X, Wg, Wu, G, U, act=name, config=config))
+    if got is None:
+        pytest.skip("not served by this kernel")
+    torch.cuda.synchronize()
+    x, wg, wu, dh, u = (v.double() for v in (X, Wg, Wu, dH, U))
+    value, slope = R.act(name, G)
+    dG, dU = dh * u * slope, dh * value
+    low = 2.0 ** -38 * float(torch.maximum((dh * u).abs(), (dh * G.double()).abs()).max())
+    eG = dG.abs() * (R.unit(t) + 2.0 ** -21) + (dh * u).abs() * R.slope_bound(name, G) + low
+    eU = dU.abs() * (R.unit(t) + 2.0 ** -21 + R.act_rel(name, G)) + low
+    for what, y, ref, err, mag, k in (
+            ("dX", got[0], dG @ wg + dU @ wu, eG @ wg.abs() + eU @ wu.abs(), dG.abs() @ wg.abs() + dU.abs() @ wu.abs(), 2 * N),
+            ("dWg", got[1], dG.T @ x, eG.T @ x.abs(), dG.abs().T @ x.abs(), M),
+            ("dWu", got[2], dU.T @ x, eU.T @ x.abs(), dU.abs().T @ x.abs(), M)):
+        assert float(ref.abs().max()) < 65504, what  # the case itself: a gradient that fp16 holds
+        bound = err * (1 + R.unit(t)) + mag * (k + 2) * 2.0 ** -24 + ref.abs() * R.unit(t) + R.tiny(t)
+        d = (y.double() - ref).abs()
+        assert bool((d <= bound).all()), (what, float((d / bound).max()))
+
+
+def test_backward_scale_with_infinities_and_zeros(dev):
+    """The scale goes by finite values: an infinite or NaN gradient leaves the
+    other tokens' dX as it is, and gradients of zeros are zeros."""
+    M, K, N = 70, 96, 130
+    X, Wg, Wu, G, U, dH = ranged_case("large", M, K, N, dev)
+    dH[3] = 0  # so the token that loses its gradient below does not hold the largest
+    clean = tlg.gated_ffn_backward(dH, X, Wg, Wu, G, U)
+    for bad in (float("inf"), float("nan")):
+        broken = dH.clone()
+        broken[3, 5] = bad
+        dX, _, _ = tlg.gated_ffn_backward(broken, X, Wg, Wu, G, U)
+        torch.cuda.synchronize()
+        others = torch.arange(M, device=dev) != 3
+        assert torch.equal(dX[others], clean[0][others])
+        assert not bool(torch.isfinite(dX[3]).any())
+    zero = tlg.gated_ffn_backward(torch.zeros_like(dH), X, Wg, Wu, G, U)
+    torch.cuda.synchronize()
+    assert all(bool((v == 0).all()) for v in zero)

@@ -37,6 +37,7 @@ struct FfnProduct {
     FfnOperand A[2], B[2];
     const float *sa;     // FFN_I8: scales of A's rows
     const float *sb[2];  // ... and of B's
+    const float *undo;   // FFN_F16 gradients: a factor of the sums (launch_ffn_gate_grad)
     void *C[3];
     int64_t ldc[3];
 };
@@ -94,10 +95,16 @@ hipError_t launch_ffn_pack(const FfnPack &p, hipStream_t stream);
 
 // dG = dH * U * act'(G) and dU = dH * act(G) for an M x N window, written as
 // two planes of M rows of `pitch` elements (a multiple of 8); columns N ..
-// pitch-1 become zero.
+// pitch-1 become zero. In fp16 both come times a power of two that the values
+// decide, and scale->undo is its reciprocal; bf16 leaves `scale` as it is.
+struct FfnGateScale {
+    static constexpr int kTops = 256;
+    uint32_t top[kTops];  // bounds of the magnitudes, by work-group
+    float undo;
+};
 hipError_t launch_ffn_gate_grad(int type, int act, int M, int N, const void *dH, int64_t lddh, const void *G,
                                 int64_t ldg, const void *U, int64_t ldu, void *dG, void *dU, int64_t pitch,
-                                const FfnPack &copies, hipStream_t stream);
+                                FfnGateScale *scale, const FfnPack &copies, hipStream_t stream);
 
 // rows x cols elements of `bytes` (2 or 4) bytes to zero.
 hipError_t launch_ffn_zero(void *p, int64_t rows, int64_t cols, int64_t ld, int bytes, hipStream_t stream);

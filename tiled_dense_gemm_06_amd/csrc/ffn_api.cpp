@@ -521,9 +521,10 @@ tlg_status gated(tlg_handle h, int32_t config, int type, int32_t out_dtype, int3
 }
 
 // The workspace of a backward pass: the dG and dU planes, rows on 128-byte
-// boundaries, then aligned copies and the parts of split sums.
+// boundaries, and their scale, then aligned copies and the parts of split sums.
 int64_t grad_pitch(int64_t N) { return round_up(N, 64); }
-int64_t planes_bytes(int64_t M, int64_t N) { return round_up(4 * M * grad_pitch(N), 256); }
+constexpr int64_t kScaleBytes = (sizeof(tlg::FfnGateScale) + 255) / 256 * 256;
+int64_t planes_bytes(int64_t M, int64_t N) { return kScaleBytes + round_up(4 * M * grad_pitch(N), 256); }
 
 tlg_status backward(tlg_handle h, int32_t config, int32_t dtype, int32_t act, const tlg_gated_ffn_grad_desc *d,
                     void *workspace, int64_t workspace_bytes, hipStream_t stream) {
@@ -556,13 +557,15 @@ tlg_status backward(tlg_handle h, int32_t config, int32_t dtype, int32_t act, co
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < tlg_gated_ffn_backward_workspace(M, N, K))
         return TLG_ERROR_INVALID_VALUE;
     const int64_t pitch = grad_pitch(N);
-    uint16_t *dG = (uint16_t *)workspace, *dU = dG + M * pitch;
+    tlg::FfnGateScale *scale = (tlg::FfnGateScale *)workspace;
+    uint16_t *dG = (uint16_t *)((char *)workspace + kScaleBytes), *dU = dG + M * pitch;
     char *ws = (char *)workspace + planes_bytes(M, N);
     const int64_t left = workspace_bytes - planes_bytes(M, N);
     const int type = type_of(dtype);
     FfnProduct px = {}, pw = {};
     px.type = pw.type = type;
     px.out_type = pw.out_type = dtype;
+    px.undo = pw.undo = &scale->undo;
     px.mode = tlg::FFN_SUM2;
     px.M = (int)M;
     px.N = (int)K;
@@ -619,7 +622,7 @@ tlg_status backward(tlg_handle h, int32_t config, int32_t dtype, int32_t act, co
         ws += bytes;
     }
     st = status_of(tlg::launch_ffn_gate_grad(type, act, (int)M, (int)N, d->dH, d->lddh, d->G, d->ldg, d->U, d->ldu, dG,
-                                             dU, pitch, k, stream));
+                                             dU, pitch, scale, k, stream));
     if (both && st == TLG_SUCCESS) {
         const auto fn = type == tlg::FFN_F16 ? tlg::launch_ffn_panel_grads_f16 : tlg::launch_ffn_panel_grads_bf16;
         // the longer sums first

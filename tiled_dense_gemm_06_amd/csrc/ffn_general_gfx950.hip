@@ -101,6 +101,11 @@ __global__ __launch_bounds__(256) void k_ffn_general(const FfnProduct p, int til
                 if (MODE == FFN_LINEAR && p.relu)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[0][e] = v[0][e] > 0.0f ? v[0][e] : 0.0f;
+                if constexpr (TYPE == FFN_F16) {
+                    const float undo = *p.undo;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[0][e] *= undo;
+                }
                 const int q = MODE == FFN_PAIR ? pair : 0;
                 ffn_store4(p.C[q], p.ldc[q], p.out_type, p.M, p.N, m, n, v[0]);
             }
@@ -130,11 +135,22 @@ __device__ __forceinline__ void pack_rows(const FfnPack &p, int w) {
 __global__ __launch_bounds__(256) void k_ffn_pack(const FfnPack p) { pack_rows(p, blockIdx.y); }
 
 // ---- gradient of the gate ----
-// One pass: dH, G and U read once, dG and dU written once, eight columns a
-// thread. Each is rounded once to the operands' type: they are matrix-core
-// operands next, and their rounding errors average out over the sums (against
-// 64 bits the gradients are 1.4 times as far off as a single final rounding,
-// one such error from dG or dU and one from the result).
+// dH, G and U read, dG and dU written, eight columns a thread. Each is rounded
+// once to the operands' type: they are matrix-core operands next, and their
+// rounding errors average out over the sums (against 64 bits the gradients are
+// 1.4 times as far off as a single final rounding, one such error from dG or
+// dU and one from the result).
+//
+// fp16 also has too few exponents: dH U act'(G) of finite values passes 65504,
+// and what is below 2^-25 is gone before the sum over tokens or channels that
+// would make it a number again. So a pass before takes the largest finite
+// |dH U| and |dH G|, which bound both gradients (every |act(g)| <= |g| and
+// |act'| < 1.13), and they are stored times the power of two that puts the bound
+// into [2^14, 2^15); the products undo it on their fp32 sums, exactly. Lost is
+// what is below 2^-38 of the largest |dH U| or |dH G|. bf16 has fp32's exponents
+// and needs none of it. Without the activation the pass is a read of three
+// matrices: 3001 x 2049 8.8 us, the backward call 112 to 124 us (130 with the
+// exact gradients in their place); 8192 x 14336 from 4096 3.14 to 3.27 ms.
 template <int TYPE>
 __device__ __forceinline__ void load8(const uint16_t *row, int n, int N, bool vec, float (&v)[8]) {
     uint32_t w[4];
@@ -151,14 +167,80 @@ __device__ __forceinline__ void load8(const uint16_t *row, int n, int N, bool ve
     for (int e = 0; e < 8; ++e) v[e] = ffn_unpack16<TYPE>((w[e / 2] >> (16 * (e % 2))) & 0xffffu);
 }
 
+// The largest of a work-group's values, in every thread.
+template <int NT>
+__device__ __forceinline__ uint32_t block_top(uint32_t top) {
+    __shared__ uint32_t part[NT / 64];
+#pragma unroll
+    for (int d = 32; d; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) top = max(top, part[i]);
+    return top;
+}
+// A magnitude's bits, ordered as integers; infinities and NaN count as 0.
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+    return b < 0x7f800000u ? b : 0;
+}
+
+// One work-group of 16 waves a CU, so that few results are left for the next
+// kernel to read; a wave takes 512 columns of a row at a time.
+constexpr int kGateTopThreads = 1024, kGateTopCols = 512;
+__global__ __launch_bounds__(kGateTopThreads) void k_ffn_gate_top(int M, int N, const uint16_t *dH, int64_t lddh,
+                                                                  const uint16_t *G, int64_t ldg, const uint16_t *U,
+                                                                  int64_t ldu, FfnGateScale *scale) {
+    const int pieces = (N - 1) / kGateTopCols + 1;  // of a row
+    const int waves = (int)gridDim.x * (kGateTopThreads / 64);
+    const int wave = (int)blockIdx.x * (kGateTopThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int rows = waves / pieces, rest = waves % pieces;
+    uint32_t by_u = 0, by_g = 0;
+    int piece = wave % pieces;
+    for (int64_t m = wave / pieces; m < M;) {
+        const int64_t n = (int64_t)piece * kGateTopCols + 8 * (threadIdx.x % 64);
+        if (n < N) {
+            float d[8], g[8], u[8];  // zeros past N
+            load8<FFN_F16>(dH + m * lddh, (int)n, N, true, d);
+            load8<FFN_F16>(G + m * ldg, (int)n, N, true, g);
+            load8<FFN_F16>(U + m * ldu, (int)n, N, true, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                by_u = max(by_u, finite_bits(d[e] * u[e]));
+                by_g = max(by_g, finite_bits(d[e] * g[e]));
+            }
+        }
+        m += rows;
+        piece += rest;
+        if (piece >= pieces) {
+            piece -= pieces;
+            ++m;
+        }
+    }
+    // a finite product of two fp16 numbers is far from fp32's end
+    const float bound = fmaxf(1.25f * __builtin_bit_cast(float, by_u), __builtin_bit_cast(float, by_g));
+    const uint32_t top = block_top<kGateTopThreads>(__builtin_bit_cast(uint32_t, bound));
+    if (threadIdx.x == 0) scale->top[blockIdx.x] = top;
+}
+
 template <int TYPE, int ACT>
 __global__ __launch_bounds__(256) void k_ffn_gate_grad(int M, int N, const uint16_t *dH, int64_t lddh,
                                                        const uint16_t *G, int64_t ldg, const uint16_t *U, int64_t ldu,
                                                        uint16_t *dG, uint16_t *dU, int64_t pitch, int chunks,
-                                                       const FfnPack copies) {
+                                                       FfnGateScale *scale, int tops, const FfnPack copies) {
     if (blockIdx.y) {
         pack_rows(copies, blockIdx.y - 1);
         return;
+    }
+    float times = 1.0f;
+    if constexpr (TYPE == FFN_F16) {
+        static_assert(FfnGateScale::kTops <= 256, "a bound a thread");
+        const uint32_t top = block_top<256>((int)threadIdx.x < tops ? scale->top[threadIdx.x] : 0);
+        // 2^14 over the bound's power of two (a product of two fp16 numbers is 2^-48 at least)
+        const int exponent = top ? (int)(top >> 23) - 127 : 14;
+        times = __builtin_bit_cast(float, (uint32_t)(127 + 14 - exponent) << 23);
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            scale->undo = __builtin_bit_cast(float, (uint32_t)(127 - 14 + exponent) << 23);
     }
     const int64_t total = (int64_t)M * chunks;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
@@ -174,8 +256,8 @@ __global__ __launch_bounds__(256) void k_ffn_gate_grad(int M, int N, const uint1
             const float value = ffn_act_grad<ACT>(g[e], &slope);
             // columns past N stay zero whatever the activation makes of 0
             const bool in = n + e < N;
-            const uint32_t bg = in ? ffn_pack16<TYPE>(d[e] * u[e] * slope) : 0;
-            const uint32_t bu = in ? ffn_pack16<TYPE>(d[e] * value) : 0;
+            const uint32_t bg = in ? ffn_pack16<TYPE>(d[e] * u[e] * slope * times) : 0;
+            const uint32_t bu = in ? ffn_pack16<TYPE>(d[e] * value * times) : 0;
             wg[e / 2] = e % 2 ? wg[e / 2] | bg << 16 : bg;
             wu[e / 2] = e % 2 ? wu[e / 2] | bu << 16 : bu;
         }
@@ -362,23 +444,33 @@ hipError_t launch_ffn_general(const FfnProduct &p, hipStream_t stream) {
 template <int TYPE, int ACT>
 static hipError_t launch_gate_grad_t(int M, int N, const void *dH, int64_t lddh, const void *G, int64_t ldg,
                                      const void *U, int64_t ldu, void *dG, void *dU, int64_t pitch,
-                                     const FfnPack &copies, hipStream_t stream) {
+                                     FfnGateScale *scale, const FfnPack &copies, hipStream_t stream) {
     const int chunks = (int)(pitch / 8);
     int64_t most = (int64_t)M * chunks;
+    int tops = 0;
+    if constexpr (TYPE == FFN_F16) {
+        const int64_t pieces = (int64_t)M * ((N - 1) / kGateTopCols + 1);
+        const int64_t groups = (pieces - 1) / (kGateTopThreads / 64) + 1;
+        tops = groups < FfnGateScale::kTops ? (int)groups : FfnGateScale::kTops;
+        hipLaunchKernelGGL(k_ffn_gate_top, dim3((unsigned)tops), dim3(kGateTopThreads), 0, stream, M, N,
+                           (const uint16_t *)dH, lddh, (const uint16_t *)G, ldg, (const uint16_t *)U, ldu, scale);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     for (int i = 0; i < copies.count; ++i)
         most = copies.rows[i] * (copies.pitch / 16) > most ? copies.rows[i] * (copies.pitch / 16) : most;
     hipLaunchKernelGGL((k_ffn_gate_grad<TYPE, ACT>), dim3(grid_for(most), 1 + (unsigned)copies.count), dim3(256), 0,
                        stream, M, N, (const uint16_t *)dH, lddh, (const uint16_t *)G, ldg, (const uint16_t *)U, ldu,
-                       (uint16_t *)dG, (uint16_t *)dU, pitch, chunks, copies);
+                       (uint16_t *)dG, (uint16_t *)dU, pitch, chunks, scale, tops, copies);
     return hipGetLastError();
 }
 
 hipError_t launch_ffn_gate_grad(int type, int act, int M, int N, const void *dH, int64_t lddh, const void *G,
                                 int64_t ldg, const void *U, int64_t ldu, void *dG, void *dU, int64_t pitch,
-                                const FfnPack &copies, hipStream_t stream) {
+                                FfnGateScale *scale, const FfnPack &copies, hipStream_t stream) {
 #define TLG_GATE_GRAD(TYPE, ACT) \
     case TYPE * 8 + ACT:           \
-        return launch_gate_grad_t<TYPE, ACT>(M, N, dH, lddh, G, ldg, U, ldu, dG, dU, pitch, copies, stream)
+        return launch_gate_grad_t<TYPE, ACT>(M, N, dH, lddh, G, ldg, U, ldu, dG, dU, pitch, scale, copies, stream)
     switch (type * 8 + act) {
         TLG_GATE_GRAD(FFN_F16, TLG_ACT_SILU);
         TLG_GATE_GRAD(FFN_F16, TLG_ACT_GELU);

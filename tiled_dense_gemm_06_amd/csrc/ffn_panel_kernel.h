@@ -406,10 +406,12 @@ __device__ __forceinline__ void panel_results(const FfnProduct &p, int out, int 
                                       });
         });
     } else {
+        const float undo = TYPE == FFN_F16 ? *p.undo : 1.0f;
         panel_store16<S, T, TYPE>(p.C[out], p.ldc[out], p.M, p.N, m, n, lane, q, [&](int tn, int tm, float (&v)[16]) {
             panel_pin(acc[tn], tm);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = acc[tn][tm + i / 4][i % 4];
+            for (int i = 0; i < 16; ++i)
+                v[i] = TYPE == FFN_F16 ? acc[tn][tm + i / 4][i % 4] * undo : acc[tn][tm + i / 4][i % 4];
         });
     }
 }
@@ -791,6 +793,11 @@ __device__ __forceinline__ void panel_join(const PanelArgs &a, int over) {
         if (MODE == FFN_LINEAR && p.relu)
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[0][e] = v[0][e] > 0.0f ? v[0][e] : 0.0f;
+        if constexpr (TYPE == FFN_F16) {
+            const float undo = *p.undo;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[0][e] *= undo;
+        }
         ffn_store4(p.C[out], p.ldc[out], p.out_type, p.M, p.N, m, n, v[0]);
     }
 }
