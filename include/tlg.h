@@ -426,7 +426,8 @@ typedef struct {
  * or description, an unknown dtype or act, negative sizes, a leading
  * dimension below the row width, a needed pointer that is NULL or not 2-byte
  * aligned, one of G and U without the other; TLG_ERROR_NOT_SUPPORTED for
- * sizes above 2^31 - 1024 or a grid of more than 2^31 - 1 work-groups. */
+ * sizes above 2^31 - 1024 or more tiles of the output (at most 256 x 128) than a
+ * launch holds, about 2^24. */
 tlg_status tlg_gated_ffn(tlg_handle h, int32_t dtype, int32_t act, const tlg_gated_ffn_desc *d, void *workspace,
                          int64_t workspace_bytes, hipStream_t stream);
 /* Workspace of a forward call: device memory, 16-byte aligned, used until the

@@ -1,8 +1,11 @@
 """Edges of the feed-forward operators that need no GPU: infinities at the end
-of a sum (tests/emu/ffn_mixed_emu.cpp)."""
+of a sum (tests/emu/ffn_mixed_emu.cpp), launches of very large problems."""
 import os
 import subprocess
 
+import pytest
+
+from tiled_dense_gemm_06_amd import _native as nat
 from tiled_dense_gemm_06_amd import build as B
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -16,3 +19,38 @@ def test_infinities_in_the_last_channels(tmp_path):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
+
+
+SHAPES = {"256x256": (256, 256), "256x128": (256, 128), "128x128": (128, 128), "64x128": (64, 128)}
+
+
+def launch_threads(product, name, splits, M, N, K):
+    """Threads of the launch that a planned kernel makes of a product."""
+    ceil = lambda a, b: -(-a // b)  # noqa: E731
+    gated = product in (nat.TLG_FFN_GATED, nat.TLG_FFN_GATED_I8)
+    rows, cols, twice = {nat.TLG_FFN_DX: (M, K, 1), nat.TLG_FFN_DW: (N, K, 2)}.get(product, (M, N, 1))
+    if name == "strip_16":
+        return ceil(cols, 16) * 512
+    if name == "general_64x64":
+        return 0  # what no kernel serves is refused by the call
+    bm, bn = SHAPES[name.split("_")[1]]
+    return (ceil(rows, bm) * ceil(cols, bn // 2 if gated else bn) * twice + (512 if splits > 1 else 0)) * 256
+
+
+@pytest.mark.parametrize("product", [nat.TLG_FFN_GATED, nat.TLG_FFN_DX, nat.TLG_FFN_DW, nat.TLG_FFN_I8,
+                                     nat.TLG_FFN_GATED_I8])
+def test_planned_launches_stay_below_2_to_the_32_threads(product):
+    sizes = [1, 8, 63, 300, 1 << 20, (1 << 24) + 1, (1 << 27) - 15, 1 << 27, (1 << 27) + 1, 1 << 30, (1 << 31) - 1024]
+    served = 0
+    for M in sizes:
+        for N in sizes:
+            for K in (1, 8, 65, 1 << 20, (1 << 27) + 1):
+                cfg, splits = nat.tlg_ffn_plan(product, M, N, K, 2, 0)
+                name = nat.tlg_ffn_config_name(cfg)
+                assert launch_threads(product, name, splits, M, N, K) < 1 << 32, (M, N, K, name)
+                served += name != "general_64x64"
+    assert served > 300
+    # few tokens against more outputs than strips, or 64-token tiles, can take
+    if product in (nat.TLG_FFN_GATED, nat.TLG_FFN_I8):
+        for N in ((1 << 27) + 1, 1 << 30):
+            assert nat.tlg_ffn_config_name(nat.tlg_ffn_plan(product, 1, N, 8, 0, 0)[0]).startswith("panel_")

@@ -163,3 +163,19 @@ def test_backward_scale_with_infinities_and_zeros(dev):
     zero = tlg.gated_ffn_backward(torch.zeros_like(dH), X, Wg, Wu, G, U)
     torch.cuda.synchronize()
     assert all(bool((v == 0).all()) for v in zero)
+
+
+@pytest.mark.parametrize("M,K", [((1 << 26) + 5, 3), ((1 << 26) + 5, 16), ((1 << 24) + 5, 1040)])
+def test_quantize_more_tokens_than_one_launch_holds(dev, M, K):
+    """Every token's codes and scale, where one launch's threads would pass 2^32."""
+    print(f"quantize {M} x {K}", flush=True)
+    base = torch.randn(997, K, generator=gen_for(dev, K), device=dev).to(torch.bfloat16)
+    rq, rs = R.quantize(base)
+    which = torch.arange(M, device=dev) % 997
+    X = base[which]
+    q, s = tlg.quantize_i8(X)
+    torch.cuda.synchronize()
+    assert torch.equal(s, rs[which])
+    step = 1 << 22
+    for m in range(0, M, step):
+        assert torch.equal(q[m:m + step], rq[which[m:m + step]]), m

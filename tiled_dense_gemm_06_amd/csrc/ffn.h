@@ -42,6 +42,9 @@ struct FfnProduct {
     int64_t ldc[3];
 };
 
+// A launch has fewer than 2^32 threads along a dimension of its grid.
+constexpr int64_t kMaxThreads = (1ll << 32) - 1;
+
 // Kernel families, and what tlg_ffn_plan reports as `config`.
 hipError_t launch_ffn_general(const FfnProduct &p, hipStream_t stream);
 

@@ -100,6 +100,10 @@ int64_t tiles_of(const Sizes &z, int shape) {
 int64_t stages_of(const Sizes &z) {
     return ceil_div(z.K, z.i8 ? 128 : 64) * (z.mode == tlg::FFN_SUM2 ? 2 : 1);
 }
+// Whether a launch holds the product's tiles (and the parts of split ones, which
+// fill the card once), or its strips of 16 outputs.
+bool tiles_fit(int64_t tiles) { return tiles <= tlg::kMaxThreads / 256 - 512; }
+bool strips_fit(const Sizes &z) { return ceil_div(z.N, 16) <= tlg::kMaxThreads / 512; }
 // Work-groups that run side by side, and the tiles that fill them in whole
 // rounds: the tiles past those may be split.
 int64_t slots_of(int shape) { return 256 * kShapes[shape].per_cu; }
@@ -275,14 +279,16 @@ int64_t plan_bytes(const Sizes &z, const Plan &p) {
 Plan plan_auto(const Sizes &z, int64_t ws_bytes) {
     Plan best = {CFG_GENERAL, 1, false};
     double least = 1e300;
-    if (forward_mode(z.mode) && z.M <= 64) {
+    if (forward_mode(z.mode) && z.M <= 64 && strips_fit(z)) {
         least = strip_time(z);
         best.cfg = CFG_SKINNY;
     }
     const double copies = z.loose ? copies_time(z, true) : 0;
     for (int shape = 0; shape < tlg::FFN_PANEL_CONFIGS; ++shape) {
         if (shape == tlg::FFN_PANEL_64x128 && !forward_mode(z.mode)) continue;
-        if (z.M <= 64 && kShapes[shape].bm > 128) continue;  // mostly rows of nothing
+        if (!tiles_fit(tiles_of(z, shape))) continue;
+        // mostly rows of nothing; but wider, where the others have too many tiles
+        if (z.M <= 64 && kShapes[shape].bm > 128 && tiles_fit(tiles_of(z, tlg::FFN_PANEL_128x128))) continue;
         const int64_t most = most_splits(z, shape);
         for (int packed = 0; packed < (z.loose ? 2 : 1); ++packed) {
             const Tiling t = tiling(z, shape, packed != 0);
@@ -312,7 +318,7 @@ void plan_both(const Sizes &zx, const Sizes &zw, Plan &x, Plan &w, int64_t ws_by
                            panel_time(tiling(zw, shape_of(w.cfg), pw), w.splits));
     for (int shape = 0; shape < tlg::FFN_PANEL_64x128; ++shape) {
         const Tiling tx = tiling(zx, shape, px), tw = tiling(zw, shape, pw);
-        if (tx.tiles + tw.tiles > 0x7fffffff) continue;
+        if (!tiles_fit(tx.tiles + tw.tiles)) continue;
         const int64_t mx = tx.whole ? 1 : most_splits(zx, shape), mw = tw.whole ? 1 : most_splits(zw, shape);
         for (int64_t sx = 1;; sx = sx * 2 < mx ? sx * 2 : mx) {
             const int64_t nx = tx.tiles * sx, kx = ceil_div(tx.stages, sx);
@@ -397,12 +403,13 @@ tlg_status choose(int32_t config, const FfnProduct &p, int64_t ws_bytes, Chosen 
     Plan &plan = o->plan;
     if (config < 0) plan = o->kmain < 0 ? Plan{CFG_GENERAL, 1, false} : plan_auto(z, ws_bytes);
     if (plan.cfg == CFG_GENERAL)
-        return ceil_div(p.M, 64) * ceil_div(p.N, 64) > 0x7fffffff ? TLG_ERROR_NOT_SUPPORTED : TLG_SUCCESS;
+        return ceil_div(p.M, 64) * ceil_div(p.N, 64) > tlg::kMaxThreads / 256 ? TLG_ERROR_NOT_SUPPORTED : TLG_SUCCESS;
     if (o->kmain < 0) return TLG_ERROR_NOT_SUPPORTED;
-    if (plan.cfg == CFG_SKINNY) return forward_mode(p.mode) && p.M <= 64 ? TLG_SUCCESS : TLG_ERROR_NOT_SUPPORTED;
+    if (plan.cfg == CFG_SKINNY)
+        return forward_mode(p.mode) && p.M <= 64 && strips_fit(z) ? TLG_SUCCESS : TLG_ERROR_NOT_SUPPORTED;
     o->shape = shape_of(plan.cfg);
     if (o->shape == tlg::FFN_PANEL_64x128 && !forward_mode(p.mode)) return TLG_ERROR_NOT_SUPPORTED;
-    if (tiles_of(z, o->shape) > 0x7fffffff) return TLG_ERROR_NOT_SUPPORTED;
+    if (!tiles_fit(tiles_of(z, o->shape))) return TLG_ERROR_NOT_SUPPORTED;
     if (config >= CFG_BOTH) {
         if (forward_mode(p.mode)) return TLG_ERROR_NOT_SUPPORTED;
         plan.splits = most_splits(z, o->shape);  // (1 for many tiles)
@@ -591,10 +598,12 @@ tlg_status backward(tlg_handle h, int32_t config, int32_t dtype, int32_t act, co
     Chosen x = {}, w = {};
     bool both = config >= CFG_BOTH;
     if (both && !(want_x && want_w)) return TLG_ERROR_NOT_SUPPORTED;
+    const auto too_many = [&] { return !tiles_fit(tiles_of(x.z, x.shape) + tiles_of(w.z, w.shape)); };
     for (int64_t room = left;; room = 0) {
         if (want_x) st = choose(config, px, room, &x);
         if (want_w && st == TLG_SUCCESS) st = choose(config, pw, room, &w);
         if (st != TLG_SUCCESS) return st;
+        if (both && too_many()) return TLG_ERROR_NOT_SUPPORTED;
         if (config < 0 && want_x && want_w && x.kmain >= 0 && w.kmain >= 0) {
             plan_both(x.z, w.z, x.plan, w.plan, room);
             both = x.plan.cfg >= CFG_BOTH;

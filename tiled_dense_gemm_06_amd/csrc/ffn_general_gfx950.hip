@@ -418,7 +418,7 @@ unsigned grid_for(int64_t items) {
 template <int TYPE, int MODE>
 hipError_t launch_general_t(const FfnProduct &p, hipStream_t stream) {
     const int64_t tm = ((int64_t)p.M + GT - 1) / GT, tn = ((int64_t)p.N + GT - 1) / GT;
-    if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
+    if (tm * tn > kMaxThreads / 256) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_ffn_general<TYPE, MODE>), dim3((unsigned)(tm * tn), MODE == FFN_PAIR ? 2 : 1), dim3(256), 0,
                        stream, p, (int)tn);
     return hipGetLastError();
@@ -491,13 +491,21 @@ static hipError_t launch_quantize_t(int64_t M, int64_t K, const void *X, int64_t
     constexpr int EB = DTYPE == TLG_F32 ? 4 : 2;
     const bool vec = K % 16 == 0 && (uintptr_t)X % 16 == 0 && ldx * EB % 16 == 0 && (uintptr_t)Q % 16 == 0 &&
                      ldq % 16 == 0;
-    if (vec)
-        hipLaunchKernelGGL((k_quantize_i8<DTYPE, NT, HELD, true>), dim3((unsigned)M), dim3(NT), 0, stream, K,
-                           (const char *)X, ldx, Q, ldq, S);
-    else
-        hipLaunchKernelGGL((k_quantize_i8<DTYPE, NT, HELD, false>), dim3((unsigned)M), dim3(NT), 0, stream, K,
-                           (const char *)X, ldx, Q, ldq, S);
-    return hipGetLastError();
+    // a launch's threads must stay below 2^32: the tokens of a longer call in several
+    constexpr int64_t most = kMaxThreads / NT;
+    hipError_t e = hipSuccess;
+    for (int64_t m = 0; m < M && e == hipSuccess; m += most) {
+        const char *x = (const char *)X + m * ldx * EB;
+        const dim3 grid((unsigned)(M - m < most ? M - m : most));
+        if (vec)
+            hipLaunchKernelGGL((k_quantize_i8<DTYPE, NT, HELD, true>), grid, dim3(NT), 0, stream, K, x, ldx,
+                               Q + m * ldq, ldq, S + m);
+        else
+            hipLaunchKernelGGL((k_quantize_i8<DTYPE, NT, HELD, false>), grid, dim3(NT), 0, stream, K, x, ldx,
+                               Q + m * ldq, ldq, S + m);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 template <int DTYPE>
