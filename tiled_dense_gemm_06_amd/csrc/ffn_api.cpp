@@ -82,6 +82,8 @@ constexpr int64_t kSplitBytes = 64ll << 20;          // partial sums of a split 
 
 constexpr int64_t kPackBytes = 1ll << 34;            // aligned copies and partial sums, at most
 
+constexpr int64_t kNever = 1ll << 60;                // more than any device has
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The sizes that a plan goes by. loose: 0, all rows of the caller's operands
@@ -128,7 +130,8 @@ int64_t pack_bytes(const Sizes &z) {
                          : z.mode == tlg::FFN_LINEAR ? z.M + z.N
                          : z.mode == tlg::FFN_SUM2   ? 2 * z.K
                                                      : z.K;
-    return rows * pack_pitch(z);
+    const int64_t pitch = pack_pitch(z);
+    return pitch && rows > kNever / pitch ? kNever : rows * pitch;
 }
 bool forward_mode(int mode) { return mode == tlg::FFN_GATED || mode == tlg::FFN_LINEAR; }
 
@@ -313,6 +316,7 @@ Plan plan_auto(const Sizes &z, int64_t ws_bytes) {
 // us, 353 x 4409 from 1117: 45 against 60; where both fill whole rounds it
 // gains nothing (8192 x 4096 from 14336: 3059 against 3008).
 void plan_both(const Sizes &zx, const Sizes &zw, Plan &x, Plan &w, int64_t ws_bytes) {
+    if (x.cfg == CFG_GENERAL || w.cfg == CFG_GENERAL) return;  // too many tiles of any shape
     const bool px = x.packed, pw = w.packed;
     double least = 0.97 * (panel_time(tiling(zx, shape_of(x.cfg), px), x.splits) +
                            panel_time(tiling(zw, shape_of(w.cfg), pw), w.splits));
@@ -349,7 +353,6 @@ void plan_both(const Sizes &zx, const Sizes &zw, Plan &x, Plan &w, int64_t ws_by
 int64_t plan_workspace(Sizes z) {
     if (z.M <= 0 || z.N <= 0 || z.K <= 0 || z.M > kMaxDim || z.N > kMaxDim || z.K > kMaxDim) return 0;
     z.loose = loose_level((forward_mode(z.mode) ? z.K : z.N) * (z.i8 ? 1 : 2));
-    if (tiles_of(z, tlg::FFN_PANEL_64x128) > 0x7fffffff) return 0;
     return plan_bytes(z, plan_auto(z, kPackBytes));
 }
 
@@ -361,12 +364,13 @@ int64_t panel_kmain(const FfnProduct &p) {
     const bool i8 = p.type == tlg::FFN_I8, acol = p.A[0].ks != 1 || p.mode == tlg::FFN_PAIR;
     const int64_t eb = i8 ? 1 : 2;
     const bool bcol = p.mode == tlg::FFN_SUM2 || p.mode == tlg::FFN_PAIR;
+    // (leading dimensions are the caller's, up to the largest int64: divided, not multiplied)
     for (int s = 0; s < (p.mode == tlg::FFN_SUM2 || p.mode == tlg::FFN_PAIR ? 2 : 1); ++s)
-        if ((acol ? 64 * p.A[s].ks : 256 * p.A[s].rs) * eb > kMaxOffset) return -1;
+        if ((acol ? p.A[s].ks : p.A[s].rs) > kMaxOffset / ((acol ? 64 : 256) * eb)) return -1;
     for (int s = 0; s < (p.mode == tlg::FFN_SUM2 || p.mode == tlg::FFN_GATED ? 2 : 1); ++s)
-        if ((bcol ? 64 * p.B[s].ks : 256 * p.B[s].rs) * eb > kMaxOffset) return -1;
+        if ((bcol ? p.B[s].ks : p.B[s].rs) > kMaxOffset / ((bcol ? 64 : 256) * eb)) return -1;
     for (int o = 0; o < 3; ++o)
-        if (p.C[o] && 128 * p.ldc[o] * 4 > kMaxOffset) return -1;
+        if (p.C[o] && p.ldc[o] > kMaxOffset / (128 * 4)) return -1;
     if (bcol) {
         if (p.N < 8) return -1;
         return tlg::pcol_kmain(p.K, p.N, p.mode == tlg::FFN_SUM2);
@@ -561,7 +565,8 @@ tlg_status backward(tlg_handle h, int32_t config, int32_t dtype, int32_t act, co
         if (want_w && e == hipSuccess) e = tlg::launch_ffn_zero(d->dWu, N, K, d->lddwu, 2, stream);
         return status_of(e);
     }
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < tlg_gated_ffn_backward_workspace(M, N, K))
+    const int64_t needed = tlg_gated_ffn_backward_workspace(M, N, K);
+    if (!workspace || !aligned(workspace, 16) || needed == INT64_MAX || workspace_bytes < needed)
         return TLG_ERROR_INVALID_VALUE;
     const int64_t pitch = grad_pitch(N);
     tlg::FfnGateScale *scale = (tlg::FfnGateScale *)workspace;
@@ -695,11 +700,9 @@ tlg_status tlg_gated_ffn_variant(tlg_handle h, int32_t config, int32_t dtype, in
 
 int64_t tlg_gated_ffn_backward_workspace(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0 || K <= 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return 0;
-    if ((uint64_t)M * (uint64_t)grad_pitch(N) > (1ull << 59)) return INT64_MAX;  // more than any device has
+    if (M > kNever / 4 / grad_pitch(N)) return INT64_MAX;
     const int loose = loose_level(2 * (uint64_t)K);
     const Sizes x = {tlg::FFN_SUM2, false, M, K, N, loose}, w = {tlg::FFN_PAIR, false, N, K, M, loose};
-    if (tiles_of(x, tlg::FFN_PANEL_128x128) > 0x7fffffff || tiles_of(w, tlg::FFN_PANEL_128x128) > 0x7fffffff)
-        return planes_bytes(M, N);
     Plan px = plan_auto(x, kPackBytes), pw = plan_auto(w, kPackBytes);
     const int64_t apart = plan_bytes(x, px) + plan_bytes(w, pw);
     plan_both(x, w, px, pw, kPackBytes);
