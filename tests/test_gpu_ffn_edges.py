@@ -179,3 +179,18 @@ def test_quantize_more_tokens_than_one_launch_holds(dev, M, K):
     step = 1 << 22
     for m in range(0, M, step):
         assert torch.equal(q[m:m + step], rq[which[m:m + step]]), m
+
+
+@pytest.mark.parametrize("config", CONFIGS, ids=config_name)
+def test_empty_sums_of_every_kernel(dev, config):
+    """K = 0: every product is +0, whichever kernel takes it; none fails."""
+    print(f"empty sums {config_name(config)}", flush=True)
+    for M, N in ((3, 5), (70, 130)):
+        h = [torch.zeros(r, 0, dtype=torch.float16, device=dev) for r in (M, N)]
+        q = [torch.zeros(r, 0, dtype=torch.int8, device=dev) for r in (M, N)]
+        s = [torch.ones(r, device=dev) for r in (M, N)]
+        outs = [served(lambda: tlg.gated_ffn(h[0], h[1], h[1], save=True, config=config)),
+                served(lambda: (tlg.gemm_i8(q[0], s[0], q[1], s[1], config=config),)),
+                served(lambda: (tlg.gated_ffn_i8(q[0], s[0], q[1], s[1], q[1], s[1], config=config),))]
+        torch.cuda.synchronize()
+        assert all(bool((v == 0).all()) and v.shape == (M, N) for o in outs if o is not None for v in o)

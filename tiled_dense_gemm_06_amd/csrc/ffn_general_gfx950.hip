@@ -531,6 +531,7 @@ hipError_t launch_quantize_i8(int dtype, int64_t M, int64_t K, const void *X, in
 hipError_t launch_ffn_pack(const FfnPack &p, hipStream_t stream) {
     int64_t most = 0;
     for (int i = 0; i < p.count; ++i) most = p.rows[i] > most ? p.rows[i] : most;
+    if (!most || !p.pitch) return hipSuccess;  // rows of no element
     hipLaunchKernelGGL(k_ffn_pack, dim3(grid_for(most * (p.pitch / 16)), (unsigned)p.count), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
