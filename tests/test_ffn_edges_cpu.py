@@ -5,6 +5,7 @@ import subprocess
 
 import pytest
 
+import tiled_dense_gemm_06_amd as tlg
 from tiled_dense_gemm_06_amd import _native as nat
 from tiled_dense_gemm_06_amd import build as B
 
@@ -54,3 +55,21 @@ def test_planned_launches_stay_below_2_to_the_32_threads(product):
     if product in (nat.TLG_FFN_GATED, nat.TLG_FFN_I8):
         for N in ((1 << 27) + 1, 1 << 30):
             assert nat.tlg_ffn_config_name(nat.tlg_ffn_plan(product, 1, N, 8, 0, 0)[0]).startswith("panel_")
+
+
+def test_forward_mode_derivatives_are_refused():
+    """... before anything else, where a result without a tangent would pass for a zero derivative."""
+    torch = pytest.importorskip("torch")
+    import torch.autograd.forward_ad as fwad
+
+    x, w = torch.zeros(4, 8, dtype=torch.float16), torch.zeros(6, 8, dtype=torch.float16)
+    with fwad.dual_level():
+        dual = fwad.make_dual(x, torch.ones_like(x))
+        for fn in (lambda: tlg.gated_ffn(dual, w, w), lambda: tlg.gated_ffn(dual, w, w, save=True),
+                   lambda: tlg.gated_ffn_backward(x, dual, w, w, x, x), lambda: tlg.quantize_i8(dual)):
+            with pytest.raises(NotImplementedError):
+                fn()
+    with pytest.raises(NotImplementedError):
+        torch.func.jvp(lambda v: tlg.gated_ffn(v, w, w), (x,), (x,))
+    with pytest.raises(NotImplementedError):
+        torch.func.vmap(lambda v: tlg.quantize_i8(v)[1])(x.expand(3, 4, 8))

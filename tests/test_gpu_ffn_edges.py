@@ -194,3 +194,42 @@ def test_empty_sums_of_every_kernel(dev, config):
                 served(lambda: (tlg.gated_ffn_i8(q[0], s[0], q[1], s[1], q[1], s[1], config=config),))]
         torch.cuda.synchronize()
         assert all(bool((v == 0).all()) and v.shape == (M, N) for o in outs if o is not None for v in o)
+
+
+def test_derivatives_that_are_not_computed_raise(dev):
+    """Forward mode, torch.func transforms and scales that require a gradient;
+    under no_grad, and detached, the same calls are served."""
+    import torch.autograd.forward_ad as fwad
+
+    X, W = torch.ones(4, 8, dtype=torch.float16, device=dev), torch.ones(6, 8, dtype=torch.float16, device=dev)
+    G = torch.ones(4, 6, dtype=torch.float16, device=dev)
+    Q, S = tlg.quantize_i8(X)
+    QW, SW = tlg.quantize_i8(W)
+    with fwad.dual_level():
+        dual = lambda v: fwad.make_dual(v, torch.ones_like(v))  # noqa: E731
+        grad = X.clone().requires_grad_()
+        for fn in (lambda: tlg.gated_ffn(dual(X), W, W), lambda: tlg.gated_ffn(X, dual(W), W),
+                   lambda: tlg.gated_ffn(X, W, dual(W), save=True), lambda: tlg.gated_ffn(grad, W, dual(W)),
+                   lambda: tlg.gated_ffn_backward(dual(G), X, W, W, G, G),
+                   lambda: tlg.gated_ffn_backward(G, X, W, W, G, dual(G)), lambda: tlg.quantize_i8(dual(X)),
+                   lambda: tlg.gemm_i8(Q, dual(S), QW, SW),
+                   lambda: tlg.gated_ffn_i8(Q, S, QW, SW, QW, dual(SW))):
+            with pytest.raises(RuntimeError):  # NotImplementedError is one, and so is autograd's own
+                fn()
+    for fn in (lambda: torch.func.jvp(lambda v: tlg.gated_ffn(v, W, W), (X,), (X,)),
+               lambda: torch.func.jvp(lambda v: tlg.gated_ffn(X, v, W), (W,), (W,)),
+               lambda: torch.func.vmap(lambda v: tlg.gated_ffn(v, W, W))(X.expand(3, 4, 8)),
+               lambda: torch.func.grad(lambda v: tlg.gated_ffn(v, W, W).float().sum())(X)):
+        with pytest.raises(RuntimeError):
+            fn()
+    for i in range(2):
+        scales = [S, SW]
+        scales[i] = scales[i].clone().requires_grad_()
+        calls = (lambda: tlg.gemm_i8(Q, scales[0], QW, scales[1]),
+                 lambda: tlg.gated_ffn_i8(Q, scales[0], QW, SW, QW, scales[1]))
+        for fn in calls:
+            with pytest.raises(NotImplementedError):
+                fn()
+            with torch.no_grad():
+                fn()
+    torch.cuda.synchronize()

@@ -7,6 +7,7 @@
 #include <ATen/DeviceGuard.h>
 #include <ATen/EmptyTensor.h>
 #include <ATen/hip/impl/HIPCachingAllocatorMasqueradingAsCUDA.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/utils/pybind.h>
@@ -49,8 +50,31 @@ int32_t dtype_of(at::ScalarType t) {
     return t == at::kHalf ? TLG_F16 : t == at::kBFloat16 ? TLG_BF16 : t == at::kFloat ? TLG_F32 : 0;
 }
 
+// Raised rather than an answer without the derivative that was asked for.
+[[noreturn]] void no_derivative(const char *name, const char *what) {
+    PyErr_SetString(PyExc_NotImplementedError, (std::string(name) + what).c_str());
+    throw py::error_already_set();
+}
+// Results carry no forward-mode derivative, and a transform's wrapper of a
+// tensor (torch.func) would come out unwrapped.
+void check_plain(const Tensor &t, const char *name) {
+    const c10::TensorImpl *impl = t.unsafeGetTensorImpl();
+    if (impl->key_set().has_any(c10::DispatchKeySet({c10::DispatchKey::FuncTorchBatched,
+                                                     c10::DispatchKey::FuncTorchGradWrapper})))
+        no_derivative(name, " belongs to a torch.func transform, which this operator has no rule for");
+    if (impl->_fw_grad(0, t).defined())
+        no_derivative(name, " carries a forward-mode derivative, which this operator does not compute");
+}
+// Scales take no gradient.
+void check_scale_grad(const Tensor &t, const char *name) {
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        no_derivative(name, " requires a gradient, which this operator does not compute (detach it, or call "
+                            "under torch.no_grad())");
+}
+
 // The operand that names the call's device and sizes.
 void check_first(const Tensor &t, const char *name, bool type_ok, const char *types) {
+    check_plain(t, name);
     if (!type_ok) type_error(name, types, t.scalar_type());
     if (t.dim() != 2) value_error(std::string(name) + " must be 2-D");
     if (!t.is_cuda()) value_error(std::string(name) + " must be on a GPU");
@@ -59,6 +83,7 @@ void check_first(const Tensor &t, const char *name, bool type_ok, const char *ty
 // Leading dimension of a row-major (rows, cols) matrix of one type on one device.
 int64_t ld_of(const Tensor &t, const char *name, at::ScalarType dtype, int64_t rows, int64_t cols,
               const at::Device &device) {
+    check_plain(t, name);
     if (t.scalar_type() != dtype) type_error(name, name_of(dtype), t.scalar_type());
     if (t.dim() != 2) value_error(std::string(name) + " must be 2-D");
     if (t.size(0) != rows || t.size(1) != cols)
@@ -74,6 +99,7 @@ int64_t ld_of(const Tensor &t, const char *name, at::ScalarType dtype, int64_t r
 }
 
 float *scales_of(const Tensor &t, const char *name, int64_t n, const at::Device &device) {
+    check_plain(t, name);
     if (t.scalar_type() != at::kFloat) type_error(name, "torch.float32", t.scalar_type());
     if (t.dim() != 1 || t.size(0) != n)
         value_error(std::string(name) + " must have " + std::to_string(n) + " elements, got " + shape_of(t));
@@ -282,6 +308,8 @@ Tensor gemm_i8(const Tensor &A, const Tensor &SA, const Tensor &B, const Tensor 
     const int64_t M = A.size(0), K = A.size(1), N = B.size(0);
     const int64_t lda = ld_of(A, "A", at::kChar, M, K, dev), ldb = ld_of(B, "B", at::kChar, N, K, dev);
     const float *sa = scales_of(SA, "SA", M, dev), *sb = scales_of(SB, "SB", N, dev);
+    check_scale_grad(SA, "SA");
+    check_scale_grad(SB, "SB");
     const auto dt = result_type(out, out_dtype, true);
     const Call call(dev, handle);
     int64_t ldc;
@@ -313,6 +341,9 @@ Tensor gated_ffn_i8(const Tensor &X, const Tensor &SX, const Tensor &Wg, const T
     d.ldg = d.ldu = N ? N : 1;
     const float *sx = scales_of(SX, "SX", M, dev), *sg = scales_of(SG, "SG", N, dev),
                 *su = scales_of(SU, "SU", N, dev);
+    check_scale_grad(SX, "SX");
+    check_scale_grad(SG, "SG");
+    check_scale_grad(SU, "SU");
     const auto dt = result_type(out, out_dtype, false);
     const Call call(dev, handle);
     Tensor H = result(out, M, N, dt, dev, &d.ldh);

@@ -13,6 +13,10 @@ device), where its results are allocated too, and returns at once; inputs of
 another stream are the caller's to order and to keep. The computation is that
 of ``libtlg.so``, reached through the compiled binding ``_ffn_torch``, which
 checks the tensors and allocates results and workspaces.
+
+Only ``gated_ffn`` takes part in autograd. Codes have no derivative;
+forward-mode derivatives, ``torch.func`` transforms and scales that require a
+gradient raise NotImplementedError.
 """
 from __future__ import annotations
 
