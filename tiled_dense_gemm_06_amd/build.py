@@ -1,6 +1,6 @@
 """Builds libtlg.so (the C-ABI library and its gfx950 kernels) in place with
-hipcc, and _ffn_torch.so (the torch binding of the feed-forward operators)
-with the host compiler.
+hipcc, and, where torch is installed, _ffn_torch.so (the torch binding of the
+feed-forward operators) with the host compiler.
 
 Each source is compiled to its own object (in parallel), then the objects are
 linked into the shared libraries.
@@ -50,9 +50,12 @@ BINDING_SOURCE = os.path.join(CSRC, "ffn_torch.cpp")
 BINDING = os.path.join(HERE, "_ffn_torch.so")
 
 
-def _binding_cmds(obj: str, out: str) -> tuple[list[str], list[str]]:
-    """The compile and the link command of the torch binding."""
-    from torch.utils import cpp_extension as ext
+def _binding_cmds(obj: str, out: str) -> tuple[list[str], list[str]] | None:
+    """The compile and the link command of the torch binding; None without torch."""
+    try:
+        from torch.utils import cpp_extension as ext
+    except ImportError:
+        return None
 
     inc = [f"-I{p}" for p in (*ext.include_paths("cuda"), sysconfig.get_paths()["include"], INCLUDE, CSRC)
            if os.path.isdir(p)]
@@ -85,16 +88,17 @@ def _compile_one(src: str, obj: str) -> subprocess.CompletedProcess:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile the library; always recompiles. Returns the path of libtlg.so."""
+    """Compile the library, and where torch is installed its binding; always
+    recompiles. Returns the path of libtlg.so, which is in place before anything
+    of the binding can fail."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     objs = [os.path.join(OBJ_DIR, os.path.basename(s) + ".o") for s in SOURCES]
     binding_obj = os.path.join(OBJ_DIR, os.path.basename(BINDING_SOURCE) + ".o")
-    binding_compile, binding_link = _binding_cmds(binding_obj, BINDING + ".tmp")
+    binding_cmds = _binding_cmds(binding_obj, BINDING + ".tmp")
     jobs = max(1, min(len(SOURCES) + 1, int(os.environ.get("MAX_JOBS", os.cpu_count() or 4))))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
-        binding = ex.submit(subprocess.run, binding_compile, capture_output=True, text=True)
+        binding = binding_cmds and ex.submit(subprocess.run, binding_cmds[0], capture_output=True, text=True)
         results = list(ex.map(_compile_one, SOURCES, objs))
-        binding = binding.result()
     for src, r in zip(SOURCES, results):
         if r.returncode != 0:
             raise RuntimeError(f"hipcc failed on {os.path.basename(src)} ({r.returncode}):\n{r.stdout}\n{r.stderr}")
@@ -106,11 +110,15 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"hipcc link failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    if binding.returncode == 0:
-        binding = subprocess.run(binding_link, capture_output=True, text=True)
-    if binding.returncode != 0:
-        raise RuntimeError(f"building {os.path.basename(BINDING)} failed ({binding.returncode}):\n{binding.stdout}\n"
-                           f"{binding.stderr}")
+    if binding is None:
+        if verbose:
+            print(f"no torch: {os.path.basename(BINDING)} is not built")
+        return LIB
+    r = binding.result()
+    if r.returncode == 0:
+        r = subprocess.run(binding_cmds[1], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building {os.path.basename(BINDING)} failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
     os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
