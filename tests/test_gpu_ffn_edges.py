@@ -233,3 +233,43 @@ def test_derivatives_that_are_not_computed_raise(dev):
             with torch.no_grad():
                 fn()
     torch.cuda.synchronize()
+
+
+def test_forward_calls_without_room_for_a_workspace(dev):
+    """Aligned copies of odd rows as large as the operands: where the allocator
+    cannot give them, the call goes on without."""
+    M, K, N = 1 << 16, 8193, 2049
+    for product in (nat.TLG_FFN_GATED, nat.TLG_FFN_I8, nat.TLG_FFN_GATED_I8):
+        assert config_name(nat.tlg_ffn_plan(product, M, N, K, 2)[0]).endswith("_packed")
+    print("no room", flush=True)
+    t = torch.bfloat16
+    g = gen_for(dev, "room")
+    # made on the GPU, kept on the host, so that no input lies in a block with room to spare
+    X, Wg, Wu = [R.exact_ints(r, K, g, dev, t, scale=0.125).cpu() for r in (M, N, N)]
+    q = [torch.randint(-127, 128, (r, K), generator=g, device=dev, dtype=torch.int8).cpu() for r in (M, N, N)]
+    torch.cuda.empty_cache()
+    X, Wg, Wu = [v.to(dev) for v in (X, Wg, Wu)]
+    q = [v.to(dev) for v in q]
+    s = [torch.rand(r, generator=g, device=dev) * 0.01 for r in (M, N, N)]
+    calls = {"gated_ffn": lambda: tlg.gated_ffn(X, Wg, Wu, act="relu"),
+             "gemm_i8": lambda: tlg.gemm_i8(q[0], s[0], q[1], s[1], out_dtype=t),
+             "gated_ffn_i8": lambda: tlg.gated_ffn_i8(q[0], s[0], q[1], s[1], q[2], s[2], act="relu", out_dtype=t)}
+    want = {k: fn().cpu() for k, fn in calls.items()}
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(dev).total_memory
+    need = [f(M, N, K) for f in (nat.lib().tlg_gated_ffn_workspace, nat.lib().tlg_gemm_i8_workspace,
+                                 nat.lib().tlg_gated_ffn_i8_workspace)]
+    assert min(need) > 3 * M * N  # (a result takes 2 M N)
+    try:
+        torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved(dev) + 3 * M * N) / total, dev)
+        with pytest.raises(torch.OutOfMemoryError):
+            torch.empty(min(need), dtype=torch.uint8, device=dev)
+        for name, fn in calls.items():
+            got = fn()
+            torch.cuda.synchronize()
+            # int8 sums are exact, and so are those of small integers
+            assert torch.equal(got.cpu(), want[name]), name
+            del got
+            torch.cuda.empty_cache()
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0, dev)

@@ -136,15 +136,22 @@ Tensor result(const OptTensor &out, int64_t rows, int64_t cols, at::ScalarType d
 }
 
 // The workspace that a call of these sizes can use; a forced kernel may take
-// up to what the largest split sum or aligned copy needs.
+// up to what the largest split sum or aligned copy needs. One that only makes
+// the call faster (a forward call's) is left out where memory does not allow
+// it: copies of unaligned operands may be as large as they are.
 constexpr int64_t kForcedWorkspace = 64ll << 20;
 struct Workspace {
     c10::DataPtr memory;
     void *p = nullptr;
     int64_t bytes = 0;
-    explicit Workspace(int64_t size) : bytes(size) {
+    explicit Workspace(int64_t size, bool needed = false) : bytes(size) {
         if (!size) return;
-        memory = allocator()->allocate((size_t)size);
+        try {
+            memory = allocator()->allocate((size_t)size);
+        } catch (const c10::OutOfMemoryError &) {
+            if (needed) throw;
+            bytes = 0;
+        }
         p = memory.get();
     }
 };
@@ -259,7 +266,7 @@ py::tuple gated_ffn_backward(const Tensor &dH, const Tensor &X, const Tensor &Wg
     }
     int64_t size = need_x || need_w ? tlg_gated_ffn_backward_workspace(M, N, K) : 0;
     if (size && config >= 0) size += kForcedWorkspace;
-    const Workspace ws(size);
+    const Workspace ws(size, true);
     call.check(tlg_gated_ffn_backward_variant(call.h, config, dtype_of(dt), act, &d, ws.p, ws.bytes, call.stream),
                "tlg_gated_ffn_backward");
     const auto some = [](bool need, const Tensor &t) { return need ? py::cast(t) : py::object(py::none()); };
