@@ -1,6 +1,7 @@
 """Edges of the feed-forward operators that need no GPU: infinities at the end
 of a sum (tests/emu/ffn_mixed_emu.cpp), launches of very large problems."""
 import os
+import re
 import subprocess
 
 import pytest
@@ -73,3 +74,19 @@ def test_forward_mode_derivatives_are_refused():
         torch.func.jvp(lambda v: tlg.gated_ffn(v, w, w), (x,), (x,))
     with pytest.raises(NotImplementedError):
         torch.func.vmap(lambda v: tlg.quantize_i8(v)[1])(x.expand(3, 4, 8))
+
+
+def test_polynomial_of_the_normal_distribution():
+    """The coefficients of ffn_phi, rounded to fp32 and evaluated in 64 bits, against erfc scaled by e^(z^2):
+    within the relative error that stands beside them."""
+    np = pytest.importorskip("numpy")
+    erfcx = pytest.importorskip("scipy.special").erfcx
+    text = open(os.path.join(B.CSRC, "ffn_ops.h")).read()
+    bound = float(re.search(r"fp32 ([0-9.e-]+) at most up to z = 31", text).group(1))
+    body = text[text.index("float ffn_phi("):]
+    body = body[:body.index("*gauss =")]
+    c = [float(np.float32(v)) for v in re.findall(r"(?:float r = |fmaf\(r, t, )(-?[0-9.]+)f", body)]
+    assert len(c) == 10 and bound < 2e-7
+    z = np.linspace(0, 31, 400001)
+    t = 1 / (1 + z / 2)
+    assert float(np.abs(t * np.polyval(c, t) / erfcx(z) - 1).max()) < bound
