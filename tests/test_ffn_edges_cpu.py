@@ -90,3 +90,19 @@ def test_polynomial_of_the_normal_distribution():
     z = np.linspace(0, 31, 400001)
     t = 1 / (1 + z / 2)
     assert float(np.abs(t * np.polyval(c, t) / erfcx(z) - 1).max()) < bound
+
+
+def test_stream_of_another_device_is_refused():
+    """A call runs on its operands' device, where such a stream is not the current one."""
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    x, w, s = torch.zeros(4, 8, dtype=torch.float16), torch.zeros(6, 8, dtype=torch.float16), torch.ones(4)
+    q, p = x.to(torch.int8), w.to(torch.int8)
+    for fn in (lambda **k: tlg.gated_ffn(x, w, w, **k), lambda **k: tlg.gated_ffn_backward(x, x, w, w, x, x, **k),
+               lambda **k: tlg.quantize_i8(x, **k), lambda **k: tlg.gemm_i8(q, s, p, s, **k),
+               lambda **k: tlg.gated_ffn_i8(q, s, p, s, p, s, **k)):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            fn(stream=Stream())

@@ -86,8 +86,8 @@ constexpr float kGeluA = 0.044715f;
 // |g| / sqrt 2 and t = 1 / (1 + z/2), erfc(z) = t e^(-z^2) R(t), where R is
 // smooth on [0, 1]; the polynomial is a least-squares fit of R at Chebyshev
 // points, weighted to even out its relative error (with these coefficients in
-// fp32 1.3e-7 at most up to z = 31, past which e^(-z^2) is zero). So Phi keeps its relative precision for
-// negative g, from one exponential and one reciprocal.
+// fp32 1.3e-7 at most up to z = 31, past which e^(-z^2) is zero). So Phi keeps
+// its relative precision for negative g, from one exponential and one reciprocal.
 __device__ __forceinline__ float ffn_phi(float g, float *gauss) {
     const float t = __builtin_amdgcn_rcpf(1.0f + 0.35355339059327376f * fabsf(g));
     float r = -0.012611449f;

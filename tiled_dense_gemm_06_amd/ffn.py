@@ -45,9 +45,13 @@ def _act(act) -> int:
     return code
 
 
-def _on(stream):
-    """The stream of a call as the current one: its results belong to it."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _on(stream, X):
+    """The stream of a call on X as the current one: its results belong to it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if stream.device != X.device:  # it would not be current where the call runs
+        raise ValueError(f"stream is on {stream.device}, the first operand on {X.device}")
+    return torch.cuda.stream(stream)
 
 
 class _GatedFFN(torch.autograd.Function):
@@ -87,7 +91,7 @@ def gated_ffn(X, Wg, Wu, *, act: str = "silu", save: bool = False, out=None, con
             (X.requires_grad or Wg.requires_grad or Wu.requires_grad))
     if stream is None and not grad:
         return _ffn_torch.gated_ffn(X, Wg, Wu, code, save, out, config, handle)
-    with _on(stream):  # autograd runs the backward pass on the stream of the forward pass
+    with _on(stream, X):  # autograd runs the backward pass on the stream of the forward pass
         if grad:
             return _GatedFFN.apply(X, Wg, Wu, code, handle)
         return _ffn_torch.gated_ffn(X, Wg, Wu, code, save, out, config, handle)
@@ -110,7 +114,7 @@ def gated_ffn_backward(dH, X, Wg, Wu, G, U, *, act: str = "silu", need_x: bool =
     tensors made within the capture): ``backward()`` inside a capture, while
     an eager graph of the same leaves is alive, is not possible with torch.
     """
-    with _on(stream):
+    with _on(stream, X):
         return _ffn_torch.gated_ffn_backward(dH, X, Wg, Wu, G, U, _act(act), need_x, need_w, config, handle)
 
 
@@ -123,7 +127,7 @@ def quantize_i8(X, *, out=None, scale=None, stream=None, handle=None):
     """
     if stream is None:
         return _ffn_torch.quantize_i8(X, out, scale, handle)
-    with _on(stream):
+    with _on(stream, X):
         return _ffn_torch.quantize_i8(X, out, scale, handle)
 
 
@@ -136,7 +140,7 @@ def gemm_i8(A, SA, B, SB, *, relu: bool = False, out=None, out_dtype=torch.float
     """
     if stream is None:
         return _ffn_torch.gemm_i8(A, SA, B, SB, relu, out, out_dtype, config, handle)
-    with _on(stream):
+    with _on(stream, A):
         return _ffn_torch.gemm_i8(A, SA, B, SB, relu, out, out_dtype, config, handle)
 
 
@@ -149,5 +153,5 @@ def gated_ffn_i8(X, SX, Wg, SG, Wu, SU, *, act: str = "silu", out=None, out_dtyp
     code = _act(act)
     if stream is None:
         return _ffn_torch.gated_ffn_i8(X, SX, Wg, SG, Wu, SU, code, out, out_dtype, config, handle)
-    with _on(stream):
+    with _on(stream, X):
         return _ffn_torch.gated_ffn_i8(X, SX, Wg, SG, Wu, SU, code, out, out_dtype, config, handle)
