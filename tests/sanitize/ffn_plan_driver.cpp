@@ -120,7 +120,7 @@ hipError_t launch_ffn_gate_grad(int, int, int M, int N, const void *, int64_t, c
     packs(copies);
     return hipSuccess;
 }
-hipError_t launch_ffn_zero(void *, int64_t, int64_t, int64_t, int, hipStream_t) { return hipSuccess; }
+hipError_t launch_ffn_zero(void *, int64_t, int64_t, int64_t, hipStream_t) { return hipSuccess; }
 }  // namespace tlg
 
 static const int64_t kSizes[] = {0, 1, 2, 7, 8, 9, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 255, 256, 257, 300, 1000,

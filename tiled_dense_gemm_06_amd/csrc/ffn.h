@@ -109,8 +109,8 @@ hipError_t launch_ffn_gate_grad(int type, int act, int M, int N, const void *dH,
                                 int64_t ldg, const void *U, int64_t ldu, void *dG, void *dU, int64_t pitch,
                                 FfnGateScale *scale, const FfnPack &copies, hipStream_t stream);
 
-// rows x cols elements of `bytes` (2 or 4) bytes to zero.
-hipError_t launch_ffn_zero(void *p, int64_t rows, int64_t cols, int64_t ld, int bytes, hipStream_t stream);
+// rows x cols elements of 16 bits to zero.
+hipError_t launch_ffn_zero(void *p, int64_t rows, int64_t cols, int64_t ld, hipStream_t stream);
 
 }  // namespace tlg
 

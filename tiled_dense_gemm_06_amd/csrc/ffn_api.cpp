@@ -560,9 +560,9 @@ tlg_status backward(tlg_handle h, int32_t config, int32_t dtype, int32_t act, co
     if (st != TLG_SUCCESS) return st;
     if (!sums) {  // M == 0: no token; N == 0: no channel
         hipError_t e = hipSuccess;
-        if (want_x) e = tlg::launch_ffn_zero(d->dX, M, K, d->lddx, 2, stream);
-        if (want_w && e == hipSuccess) e = tlg::launch_ffn_zero(d->dWg, N, K, d->lddwg, 2, stream);
-        if (want_w && e == hipSuccess) e = tlg::launch_ffn_zero(d->dWu, N, K, d->lddwu, 2, stream);
+        if (want_x) e = tlg::launch_ffn_zero(d->dX, M, K, d->lddx, stream);
+        if (want_w && e == hipSuccess) e = tlg::launch_ffn_zero(d->dWg, N, K, d->lddwg, stream);
+        if (want_w && e == hipSuccess) e = tlg::launch_ffn_zero(d->dWu, N, K, d->lddwu, stream);
         return status_of(e);
     }
     const int64_t needed = tlg_gated_ffn_backward_workspace(M, N, K);

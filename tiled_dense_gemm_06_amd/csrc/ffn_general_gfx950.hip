@@ -152,9 +152,9 @@ __global__ __launch_bounds__(256) void k_ffn_pack(const FfnPack p) { pack_rows(p
 // matrices: 3001 x 2049 8.8 us, the backward call 112 to 124 us (130 with the
 // exact gradients in their place); 8192 x 14336 from 4096 3.14 to 3.27 ms.
 template <int TYPE>
-__device__ __forceinline__ void load8(const uint16_t *row, int n, int N, bool vec, float (&v)[8]) {
+__device__ __forceinline__ void load8(const uint16_t *row, int n, int N, float (&v)[8]) {
     uint32_t w[4];
-    if (vec && n + 8 <= N) {
+    if (n + 8 <= N) {
         __builtin_memcpy(w, row + n, 16);
     } else {
 #pragma unroll
@@ -201,9 +201,9 @@ __global__ __launch_bounds__(kGateTopThreads) void k_ffn_gate_top(int M, int N, 
         const int64_t n = (int64_t)piece * kGateTopCols + 8 * (threadIdx.x % 64);
         if (n < N) {
             float d[8], g[8], u[8];  // zeros past N
-            load8<FFN_F16>(dH + m * lddh, (int)n, N, true, d);
-            load8<FFN_F16>(G + m * ldg, (int)n, N, true, g);
-            load8<FFN_F16>(U + m * ldu, (int)n, N, true, u);
+            load8<FFN_F16>(dH + m * lddh, (int)n, N, d);
+            load8<FFN_F16>(G + m * ldg, (int)n, N, g);
+            load8<FFN_F16>(U + m * ldu, (int)n, N, u);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 by_u = max(by_u, finite_bits(d[e] * u[e]));
@@ -246,9 +246,9 @@ __global__ __launch_bounds__(256) void k_ffn_gate_grad(int M, int N, const uint1
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int m = (int)(i / chunks), n = (int)(i % chunks) * 8;
         float d[8], g[8], u[8];
-        load8<TYPE>(dH + (int64_t)m * lddh, n, N, true, d);
-        load8<TYPE>(G + (int64_t)m * ldg, n, N, true, g);
-        load8<TYPE>(U + (int64_t)m * ldu, n, N, true, u);
+        load8<TYPE>(dH + (int64_t)m * lddh, n, N, d);
+        load8<TYPE>(G + (int64_t)m * ldg, n, N, g);
+        load8<TYPE>(U + (int64_t)m * ldu, n, N, u);
         uint32_t wg[4], wu[4];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -398,16 +398,10 @@ __global__ __launch_bounds__(NT) void k_quantize_i8(int64_t K, const char *X, in
     }
 }
 
-template <int BYTES>
-__global__ __launch_bounds__(256) void k_ffn_zero(char *p, int64_t rows, int64_t cols, int64_t ld) {
+__global__ __launch_bounds__(256) void k_ffn_zero(uint16_t *p, int64_t rows, int64_t cols, int64_t ld) {
     const int64_t total = rows * cols;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        char *at = p + ((i / cols) * ld + i % cols) * BYTES;
-        if (BYTES == 4)
-            *(uint32_t *)at = 0;
-        else
-            *(uint16_t *)at = 0;
-    }
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256)
+        p[i / cols * ld + i % cols] = 0;
 }
 
 unsigned grid_for(int64_t items) {
@@ -536,13 +530,9 @@ hipError_t launch_ffn_pack(const FfnPack &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_ffn_zero(void *p, int64_t rows, int64_t cols, int64_t ld, int bytes, hipStream_t stream) {
+hipError_t launch_ffn_zero(void *p, int64_t rows, int64_t cols, int64_t ld, hipStream_t stream) {
     if (rows <= 0 || cols <= 0) return hipSuccess;
-    const unsigned grid = grid_for(rows * cols);
-    if (bytes == 4)
-        hipLaunchKernelGGL(k_ffn_zero<4>, dim3(grid), dim3(256), 0, stream, (char *)p, rows, cols, ld);
-    else
-        hipLaunchKernelGGL(k_ffn_zero<2>, dim3(grid), dim3(256), 0, stream, (char *)p, rows, cols, ld);
+    hipLaunchKernelGGL(k_ffn_zero, dim3(grid_for(rows * cols)), dim3(256), 0, stream, (uint16_t *)p, rows, cols, ld);
     return hipGetLastError();
 }
 

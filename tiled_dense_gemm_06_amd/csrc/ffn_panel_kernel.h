@@ -43,7 +43,7 @@ struct PanelArgs : FfnPanelCall {
 };
 
 // The work of a launch: `whole` tiles, then the parts of the others.
-template <class S, int MODE>
+template <int MODE>
 __host__ __device__ __forceinline__ int panel_tile_rows(const PanelArgs &a) {
     return MODE == FFN_PAIR ? 2 * a.tiles_m : a.tiles_m;  // the pair's second output follows the first's rows
 }
@@ -437,7 +437,7 @@ __device__ __forceinline__ void panel_product(const PanelArgs &a, const int bloc
     const FfnProduct &p = a.p;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm0 = (wave / S::WN) * S::WTM, wn0 = (wave % S::WN) * S::WTN;
-    const int rows_of_tiles = panel_tile_rows<S, MODE>(a);
+    const int rows_of_tiles = panel_tile_rows<MODE>(a);
     const bool split = block >= a.whole;
     const int over = block - a.whole;
     const int tile = split ? a.whole + over / a.splits : xcd_remap(block, a.whole);
@@ -743,7 +743,7 @@ __device__ __forceinline__ void panel_join(const PanelArgs &a, int over) {
     constexpr int NB = MODE == FFN_GATED ? 2 : 1, BNOUT = S::BN / NB, QUADS = BNOUT / 4;
     const FfnProduct &p = a.p;
     int tm_idx, tn_idx;
-    grouped_tile(a.whole + over, panel_tile_rows<S, MODE>(a), a.tiles_n, a.group_m, &tm_idx, &tn_idx);
+    grouped_tile(a.whole + over, panel_tile_rows<MODE>(a), a.tiles_n, a.group_m, &tm_idx, &tn_idx);
     const int out = MODE == FFN_PAIR && tm_idx >= a.tiles_m ? 1 : 0;
     if (out) tm_idx -= a.tiles_m;
     const int rows = panel_part_rows<S>(a), i = blockIdx.x * 256 + threadIdx.x;
@@ -833,7 +833,7 @@ struct PanelGrid {
         const int n = MODE == FFN_GATED ? S::BN / 2 : S::BN;
         a.tiles_m = (a.p.M + S::BM - 1) / S::BM;
         a.tiles_n = (a.p.N + n - 1) / n;
-        tiles = panel_tile_rows<S, MODE>(a) * a.tiles_n;
+        tiles = panel_tile_rows<MODE>(a) * a.tiles_n;
         if (a.splits < 2) a.whole = tiles;
     }
     unsigned groups() const { return (unsigned)(a.whole + (tiles - a.whole) * a.splits); }

@@ -21,7 +21,6 @@ namespace tlg {
 
 namespace {
 
-template <int EB>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t skinny_rsrc(const void *base) {
     return __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, (int)kRange, 0x00020000);
 }
@@ -29,40 +28,36 @@ __device__ __forceinline__ int4_t skinny_load(__amdgpu_buffer_rsrc_t r, uint32_t
     return __builtin_bit_cast(int4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-// TM tiles of 16 tokens, TN tiles of 16 outputs, K split over WAVES waves.
-template <int TYPE, int MODE, int TM, int TN, int WAVES>
+// TM tiles of 16 tokens, 16 outputs, K split over WAVES waves.
+template <int TYPE, int MODE, int TM, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void k_ffn_skinny(const FfnProduct p, int kmain) {
     using T = FfnT<TYPE>;
     using Acc = typename T::Acc;
     using E = typename T::Elem;
     constexpr int EB = T::EB, NB = MODE == FFN_GATED ? 2 : 1, J = 4;  // J loads: 256 bytes of a row
     constexpr int BK = J * 64 / EB, PER = 16 / EB;
-    __shared__ Acc part[WAVES][NB * TN * TM][64];
+    __shared__ Acc part[WAVES][NB * TM][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane % 16, g = lane / 16;
-    const int64_t n0 = (int64_t)blockIdx.x * (16 * TN);
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
 
     // rows past the last one read the last one again; their sums are not stored
-    uint32_t offa[TM], offb[NB][TN];
+    uint32_t offa[TM], offb[NB];
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
         const int m = 16 * t + r;
         offa[t] = (uint32_t)((m < p.M ? m : p.M - 1) * p.A[0].rs * EB + 16 * g);
     }
+    const int64_t last = p.N - 1 - n0;
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int t = 0; t < TN; ++t) {
-            const int64_t n = 16 * t + r, last = p.N - 1 - n0;
-            offb[b][t] = (uint32_t)((n < last ? n : last) * p.B[b].rs * EB + 16 * g);
-        }
-    const __amdgpu_buffer_rsrc_t ra = skinny_rsrc<EB>(p.A[0].p);
+    for (int b = 0; b < NB; ++b) offb[b] = (uint32_t)((r < last ? r : last) * p.B[b].rs * EB + 16 * g);
+    const __amdgpu_buffer_rsrc_t ra = skinny_rsrc(p.A[0].p);
     __amdgpu_buffer_rsrc_t rb[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) rb[b] = skinny_rsrc<EB>((const char *)p.B[b].p + n0 * p.B[b].rs * EB);
+    for (int b = 0; b < NB; ++b) rb[b] = skinny_rsrc((const char *)p.B[b].p + n0 * p.B[b].rs * EB);
 
     struct Block {
-        int4_t a[TM][J], b[NB][TN][J];
+        int4_t a[TM][J], b[NB][J];
     };
     // Block `i` of K; a lane whose 16 bytes start at or past kmain gets zeros.
     auto load = [&](Block &x, int i) {
@@ -72,29 +67,23 @@ __global__ __launch_bounds__(WAVES * 64) void k_ffn_skinny(const FfnProduct p, i
             const bool in = k + g * PER < kmain;
             const uint32_t at = (uint32_t)(k * EB);
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int t = 0; t < TN; ++t) x.b[b][t][j] = skinny_load(rb[b], in ? offb[b][t] + at : kOOB);
+            for (int b = 0; b < NB; ++b) x.b[b][j] = skinny_load(rb[b], in ? offb[b] + at : kOOB);
 #pragma unroll
             for (int t = 0; t < TM; ++t) x.a[t][j] = skinny_load(ra, in ? offa[t] + at : kOOB);
         }
     };
-    Acc acc[NB][TN][TM];
+    Acc acc[NB][TM];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int t = 0; t < TN; ++t)
-#pragma unroll
-            for (int m = 0; m < TM; ++m) acc[b][t][m] = Acc{0, 0, 0, 0};
+        for (int m = 0; m < TM; ++m) acc[b][m] = Acc{0, 0, 0, 0};
     auto multiply = [&](const Block &x) {
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int t = 0; t < TN; ++t)
-#pragma unroll
-                    for (int m = 0; m < TM; ++m) acc[b][t][m] = T::mfma(x.b[b][t][j], x.a[m][j], acc[b][t][m]);
+                for (int m = 0; m < TM; ++m) acc[b][m] = T::mfma(x.b[b][j], x.a[m][j], acc[b][m]);
     };
     // (a start of its own for every strip, as the 64-token tiles have, costs
     // here: 1 token 4096 -> 14336 43.8 against 42.8 us; the waves' blocks
@@ -128,32 +117,26 @@ __global__ __launch_bounds__(WAVES * 64) void k_ffn_skinny(const FfnProduct p, i
             y.a[t][0] = tail(p.A[0].p, m < p.M ? m : p.M - 1, p.A[0].rs);
         }
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < NB; ++b) {
+            y.b[b][0] = tail(p.B[b].p, n0 + (r < last ? r : last), p.B[b].rs);
 #pragma unroll
-            for (int t = 0; t < TN; ++t) {
-                const int64_t n = n0 + 16 * t + r;
-                y.b[b][t][0] = tail(p.B[b].p, n < p.N ? n : p.N - 1, p.B[b].rs);
-#pragma unroll
-                for (int m = 0; m < TM; ++m) acc[b][t][m] = T::mfma(y.b[b][t][0], y.a[m][0], acc[b][t][m]);
-            }
+            for (int m = 0; m < TM; ++m) acc[b][m] = T::mfma(y.b[b][0], y.a[m][0], acc[b][m]);
+        }
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int t = 0; t < TN; ++t)
-#pragma unroll
-            for (int m = 0; m < TM; ++m) part[wave][(b * TN + t) * TM + m][lane] = acc[b][t][m];
+        for (int m = 0; m < TM; ++m) part[wave][b * TM + m][lane] = acc[b][m];
     __syncthreads();
-    // lane l: token 16 * tm + l % 16, outputs 4 * (l / 16) .. +3 of its tile
-    for (int i = wave; i < TN * TM; i += WAVES) {
-        const int t = i / TM, m = i % TM;
-        const int row = 16 * m + r, col = (int)n0 + 16 * t + 4 * g;
+    // lane l: token 16 * m + l % 16, outputs 4 * (l / 16) .. +3
+    for (int m = wave; m < TM; m += WAVES) {
+        const int row = 16 * m + r, col = (int)n0 + 4 * g;
         float v[NB][4];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            Acc s = part[0][(b * TN + t) * TM + m][lane];
+            Acc s = part[0][b * TM + m][lane];
 #pragma unroll
-            for (int w = 1; w < WAVES; ++w) s += part[w][(b * TN + t) * TM + m][lane];
+            for (int w = 1; w < WAVES; ++w) s += part[w][b * TM + m][lane];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 v[b][e] = (float)s[e];
@@ -181,10 +164,10 @@ __global__ __launch_bounds__(WAVES * 64) void k_ffn_skinny(const FfnProduct p, i
     }
 }
 
-template <int TYPE, int MODE, int TM, int TN, int WAVES>
+template <int TYPE, int MODE, int TM, int WAVES>
 hipError_t launch_t(const FfnProduct &p, int kmain, hipStream_t stream) {
-    const unsigned strips = (unsigned)(((int64_t)p.N + 16 * TN - 1) / (16 * TN));
-    hipLaunchKernelGGL((k_ffn_skinny<TYPE, MODE, TM, TN, WAVES>), dim3(strips), dim3(WAVES * 64), 0, stream, p,
+    const unsigned strips = (unsigned)(((int64_t)p.N + 15) / 16);
+    hipLaunchKernelGGL((k_ffn_skinny<TYPE, MODE, TM, WAVES>), dim3(strips), dim3(WAVES * 64), 0, stream, p,
                        kmain);
     return hipGetLastError();
 }
@@ -193,10 +176,10 @@ template <int TYPE, int MODE>
 hipError_t launch_rows(const FfnProduct &p, int kmain, hipStream_t stream) {
     const int tm = (p.M + 15) / 16;
     switch (tm) {
-        case 1: return launch_t<TYPE, MODE, 1, 1, 8>(p, kmain, stream);
-        case 2: return launch_t<TYPE, MODE, 2, 1, 8>(p, kmain, stream);
+        case 1: return launch_t<TYPE, MODE, 1, 8>(p, kmain, stream);
+        case 2: return launch_t<TYPE, MODE, 2, 8>(p, kmain, stream);
         case 3:
-        case 4: return launch_t<TYPE, MODE, 4, 1, 8>(p, kmain, stream);
+        case 4: return launch_t<TYPE, MODE, 4, 8>(p, kmain, stream);
         default: return hipErrorInvalidValue;
     }
 }
