@@ -273,3 +273,54 @@ def test_forward_calls_without_room_for_a_workspace(dev):
             torch.cuda.empty_cache()
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0, dev)
+
+
+@pytest.mark.parametrize("config", CONFIGS, ids=config_name)
+@pytest.mark.parametrize("t", T16, ids=["fp16", "bf16"])
+def test_backward_nan_stays_in_its_token_and_channel(dev, t, config):
+    """A NaN in one token's dH spoils that token's dX and that channel's weight gradients, nothing else."""
+    M, K, N = 150, 77, 131
+    print(f"nan {t} {config_name(config)}", flush=True)
+    g = gen_for(dev, "nan", M)
+    X = R.exact_ints(M, K, g, dev, t)
+    Wg, Wu = (R.exact_ints(N, K, g, dev, t) for _ in range(2))
+    G, U, dH = (R.exact_ints(M, N, g, dev, t) for _ in range(3))
+    clean = served(lambda: tlg.gated_ffn_backward(dH, X, Wg, Wu, G, U, act="relu", config=config))
+    if clean is None:
+        pytest.skip("not served by this kernel")
+    for m, n in ((0, 0), (M - 1, N - 1), (64, 128)):
+        bad = dH.clone()
+        bad[m, n] = float("nan")
+        dX, dWg, dWu = tlg.gated_ffn_backward(bad, X, Wg, Wu, G, U, act="relu", config=config)
+        torch.cuda.synchronize()
+        rows, cols = torch.arange(M, device=dev) != m, torch.arange(N, device=dev) != n
+        assert bool(torch.isnan(dX[m]).all()) and bool(torch.isnan(dWg[n]).all()) and bool(torch.isnan(dWu[n]).all())
+        assert torch.equal(dX[rows], clean[0][rows])
+        assert torch.equal(dWg[cols], clean[1][cols]) and torch.equal(dWu[cols], clean[2][cols])
+
+
+def test_graph_replays_of_the_fp16_backward_pass(dev):
+    """The scale of dG and dU is found anew by every replay: gradients of other
+    magnitudes from one to the next, eager calls between them."""
+    M, K, N = 96, 136, 200
+    X, Wg, Wu, G, U, dH = ranged_case("large", M, K, N, dev)
+    step = lambda: tlg.gated_ffn_backward(dH, X, Wg, Wu, G, U)  # noqa: E731
+    side = torch.cuda.Stream(dev)
+    side.wait_stream(torch.cuda.current_stream(dev))
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream(dev).wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    g = gen_for(dev, "replays")
+    for scale in (256, 1e-6, 1, 0, 256):
+        dH.copy_(torch.randn(M, N, generator=g, device=dev) * scale)
+        for o in outs:
+            o.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, step()):
+            assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+        torch.cuda.synchronize()
