@@ -433,7 +433,8 @@ tlg_status tlg_gated_ffn(tlg_handle h, int32_t dtype, int32_t act, const tlg_gat
 /* Workspace of a forward call: device memory, 16-byte aligned, used until the
  * call's work on the stream has ended. It is optional (NULL and 0): with at
  * least as many bytes as the call's _workspace function says, few large sums
- * are cut into parts that run side by side (added in a fixed order). */
+ * are cut into parts that run side by side (added in a fixed order), and rows
+ * that start off 128-byte lines are copied onto them where that is faster. */
 int64_t tlg_gated_ffn_workspace(int64_t M, int64_t N, int64_t K);
 
 /* Backward pass of tlg_gated_ffn: from dH (M, N), the inputs and the kept G

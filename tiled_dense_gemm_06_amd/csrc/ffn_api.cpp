@@ -61,7 +61,8 @@ enum {
 // example: 256 x 256, 224 tiles of 64 stages 97; 256 x 128, 224 tiles 72; 128 x
 // 128, 448 tiles 82 in pairs; deep, 224 tiles 55; 64 x 128, 32 tiles of 112
 // stages 44; 192 tiles of 256 x 256 of one stage 13. On 210 random problems
-// of the operators' ranges the choice took 1.006 times the best kernel's time.
+// of the operators' ranges, every kernel forced, the choice took 1.006 times the
+// best one's time.
 struct Shape {
     const char *name, *split_name, *packed_name, *both_name;
     int bm, bn;

@@ -19,8 +19,9 @@
 // product the tile's 256 rows of B are 128 of Wg and 128 of Wu, alternating so
 // that each wave has both sums of the same outputs in its registers.
 // K's end is masked in the loads (a lane past it gets zeros), so the last
-// stage needs no other code; only the elements past the last whole 16-byte
-// chunk (K no multiple of 8 elements of 16 bits, 16 of 8 bits) are staged one
+// stage needs no other code; only what is left past the last whole 16-byte
+// chunk (K no multiple of 8 elements of 16 bits, 16 of 8 bits), or past the rows
+// that a column-layout operand's chunks may cross (pcol_kmain), is staged one
 // by one after the loop.
 #ifndef TLG_FFN_PANEL_KERNEL_H
 #define TLG_FFN_PANEL_KERNEL_H
