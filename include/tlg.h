@@ -442,9 +442,9 @@ int64_t tlg_gated_ffn_workspace(int64_t M, int64_t N, int64_t K);
  * dtype, as operands of the products):
  *   dX = dG Wg + dU Wu (M, K),  dWg = dG^T X,  dWu = dU^T X (N, K).
  * In TLG_F16 dG and dU are rounded at a scale of their own, a power of two from
- * the largest finite |dH U| and |dH G| of the call that is undone on the fp32
- * sums: no finite dG or dU overflows, and what is lost of them is below 2^-38
- * of the larger.
+ * the largest finite |dH U| and |dH G| (at most 0.28 |dH| where G < 0) of the
+ * call that is undone on the fp32 sums: no finite dG or dU overflows, and what
+ * is lost of them is below 2^-38 of the larger.
  * dX, and dWg and dWu together, may be NULL: not computed, and what only they
  * need (Wg and Wu; X) may then be NULL too. Empty sums give zeros. A gradient
  * taken alone may be summed (in fp32) in another order than with the others. */

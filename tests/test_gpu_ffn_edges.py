@@ -324,3 +324,33 @@ def test_graph_replays_of_the_fp16_backward_pass(dev):
         for a, b in zip(outs, step()):
             assert torch.equal(a, b) and bool(torch.isfinite(a).all())
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh", "relu"])
+def test_closed_gates_do_not_set_the_scale(dev, name):
+    """A far negative gate passes nothing on, so it takes nothing from the
+    precision of the others: bounds as above, with |dH G| at most 0.28 |dH|
+    where G < 0."""
+    M, K, N = 130, 77, 90
+    t = torch.float16
+    g = gen_for(dev, "closed", name)
+    X, Wg, Wu = (torch.randn(r, K, generator=g, device=dev).to(t) for r in (M, N, N))
+    G = torch.randn(M, N, generator=g, device=dev).to(t)
+    U, dH = ((torch.randn(M, N, generator=g, device=dev) * s).to(t) for s in (1, 1e-6))
+    G[7, 5], dH[7, 5], U[7, 5] = -60000, 1, 1e-7
+    dX, dWg, dWu = tlg.gated_ffn_backward(dH, X, Wg, Wu, G, U, act=name)
+    torch.cuda.synchronize()
+    x, wg, wu, dh, u, g64 = (v.double() for v in (X, Wg, Wu, dH, U, G))
+    value, slope = R.act(name, G)
+    dG, dU = dh * u * slope, dh * value
+    gate = torch.where(g64 > 0, g64, (-g64).clamp(max=0.28))
+    low = 2.0 ** -38 * float(torch.maximum((dh * u).abs(), dh.abs() * gate).max())
+    eG = dG.abs() * (R.unit(t) + 2.0 ** -21) + (dh * u).abs() * R.slope_bound(name, G) + low
+    eU = dU.abs() * (R.unit(t) + 2.0 ** -21 + R.act_rel(name, G)) + low
+    for what, y, ref, err, mag, k in (
+            ("dX", dX, dG @ wg + dU @ wu, eG @ wg.abs() + eU @ wu.abs(), dG.abs() @ wg.abs() + dU.abs() @ wu.abs(), 2 * N),
+            ("dWg", dWg, dG.T @ x, eG.T @ x.abs(), dG.abs().T @ x.abs(), M),
+            ("dWu", dWu, dU.T @ x, eU.T @ x.abs(), dU.abs().T @ x.abs(), M)):
+        bound = err * (1 + R.unit(t)) + mag * (k + 2) * 2.0 ** -24 + ref.abs() * R.unit(t) + R.tiny(t)
+        d = (y.double() - ref).abs()
+        assert bool((d <= bound).all()), (what, float((d / bound).max()))

@@ -144,11 +144,12 @@ __global__ __launch_bounds__(256) void k_ffn_pack(const FfnPack p) { pack_rows(p
 // fp16 also has too few exponents: dH U act'(G) of finite values passes 65504,
 // and what is below 2^-25 is gone before the sum over tokens or channels that
 // would make it a number again. So a pass before takes the largest finite
-// |dH U| and |dH G|, which bound both gradients (every |act(g)| <= |g| and
-// |act'| < 1.13), and they are stored times the power of two that puts the bound
+// |dH U| and |dH a(G)|, a(g) = g for g > 0 and min(|g|, 0.28) for the others,
+// which bound both gradients (|act(g)| <= a(g) and |act'| < 1.13 for every
+// activation), and they are stored times the power of two that puts the bound
 // into [2^14, 2^15); the products undo it on their fp32 sums, exactly. Lost is
-// what is below 2^-38 of the largest |dH U| or |dH G|. bf16 has fp32's exponents
-// and needs none of it. Without the activation the pass is a read of three
+// what is below 2^-38 of the largest |dH U| or |dH a(G)|. bf16 has fp32's
+// exponents and needs none of it. Without the activation the pass is a read of three
 // matrices: 3001 x 2049 8.8 us, the backward call 112 to 124 us (130 with the
 // exact gradients in their place); 8192 x 14336 from 4096 3.14 to 3.27 ms.
 template <int TYPE>
@@ -207,7 +208,7 @@ __global__ __launch_bounds__(kGateTopThreads) void k_ffn_gate_top(int M, int N, 
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 by_u = max(by_u, finite_bits(d[e] * u[e]));
-                by_g = max(by_g, finite_bits(d[e] * g[e]));
+                by_g = max(by_g, finite_bits(d[e] * fmaxf(g[e], fminf(-g[e], 0.28f))));
             }
         }
         m += rows;

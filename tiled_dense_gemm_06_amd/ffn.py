@@ -106,9 +106,10 @@ def gated_ffn_backward(dH, X, Wg, Wu, G, U, *, act: str = "silu", need_x: bool =
     of its fp32 sums. dG and dU, the gradients of the two products, are
     rounded to the inputs' type on the way (the products' operands); in fp16
     at a power of two of their own, so that none overflows and only what is
-    below 2^-38 of the largest |dH U| or |dH G| is lost. They live in a workspace from torch's
-    allocator: 4 M bytes times N rounded up to 64, and what copies of
-    unaligned rows and split sums take.
+    below 2^-38 of the largest |dH U| or |dH G| (at most 0.28 |dH| where
+    G < 0) is lost. They live in a workspace from torch's allocator: 4 M bytes
+    times N rounded up to 64, and what copies of unaligned rows and split sums
+    take.
 
     In a graph capture call this function (or ``torch.autograd.grad`` on
     tensors made within the capture): ``backward()`` inside a capture, while
